@@ -60,6 +60,26 @@ class s2r_params(ctypes.Structure):
         }
 
 
+S2R_BF16, S2R_F16, S2R_F32 = range(3)
+S2R_E4M3, S2R_E5M2 = range(2)
+S2R_ACT_SILU, S2R_ACT_GELU, S2R_ACT_GELU_TANH = range(3)
+_FORMATS = {"e4m3": S2R_E4M3, "e5m2": S2R_E5M2}
+_ACTS = {"silu": S2R_ACT_SILU, "gelu": S2R_ACT_GELU, "gelu_tanh": S2R_ACT_GELU_TANH}
+
+
+class s2r_mat(ctypes.Structure):
+    """Mirror of ``s2r_mat`` in include/s2r_q8.h; made from a tensor by mat()."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("dtype", ctypes.c_uint32)]
+
+
+class s2r_q8_mat(ctypes.Structure):
+    """Mirror of ``s2r_q8_mat`` in include/s2r_q8.h; made from tensors by q8_mat() or alloc_q8()."""
+
+    _fields_ = [("q", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("scale", ctypes.c_void_p),
+                ("lds", ctypes.c_uint64), ("format", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -115,6 +135,21 @@ def lib() -> ctypes.CDLL:
         L.s2r_diag_stream_write.restype = st
         L.s2r_diag_stream_read.argtypes = [vp, sz, vp, vp]
         L.s2r_diag_stream_read.restype = st
+        pm, pq = P(s2r_mat), P(s2r_q8_mat)
+        L.s2r_q8_save.argtypes = [u64, u64, pm, pq, vp]
+        L.s2r_q8_load.argtypes = [u64, u64, pq, pm, vp]
+        L.s2r_q8_weight.argtypes = [u64, u64, pm, pq, pq, vp]
+        L.s2r_q8_gemm_workspace_bytes.argtypes = [u64, u64, u64]
+        L.s2r_q8_gemm_workspace_bytes.restype = sz
+        L.s2r_q8_gemm.argtypes = [u64, u64, u64, pq, pq, pm, vp, sz, vp]
+        L.s2r_q8_wgrad_workspace_bytes.argtypes = [u64, u64, u64]
+        L.s2r_q8_wgrad_workspace_bytes.restype = sz
+        L.s2r_q8_wgrad.argtypes = [u64, u64, u64, pm, pq, pq, vp, u64, ctypes.c_int, vp, sz, vp]
+        L.s2r_q8_glu.argtypes = [u64, u64, ctypes.c_int, pm, pm, pq, pq, pm, pq, vp]
+        L.s2r_q8_glu_grad.argtypes = [u64, u64, ctypes.c_int, pq, pq, pm, pm, pm, pq, pq, vp]
+        for f in (L.s2r_q8_save, L.s2r_q8_load, L.s2r_q8_weight, L.s2r_q8_gemm, L.s2r_q8_wgrad,
+                  L.s2r_q8_glu, L.s2r_q8_glu_grad):
+            f.restype = st
         L.s2r_status_string.argtypes = [st]
         L.s2r_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -255,6 +290,125 @@ def s2r_topk_ef(W: int, grad, residual, n: int, ld: int, block: int, K: int, out
            "s2r_topk_ef")
 
 
+# ---------------------------------------------------------------------------------------
+# training in 8 bits (include/s2r_q8.h)
+
+
+def mat(t) -> s2r_mat:
+    """Descriptor of a 2-D bf16, fp16 or fp32 tensor with unit stride along its rows; keeps
+    the tensor alive."""
+    import torch
+    codes = {torch.bfloat16: S2R_BF16, torch.float16: S2R_F16, torch.float32: S2R_F32}
+    if t.dim() != 2 or t.dtype not in codes or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise S2RError(S2R_ERR_DIM, "mat")
+    ld = max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    m = s2r_mat(t.data_ptr(), ld, codes[t.dtype])
+    m.tensor = t
+    return m
+
+
+def q8_mat(q, scale, fmt: str = "e4m3") -> s2r_q8_mat:
+    """Descriptor of an 8-bit matrix: q [rows][ld] and scale [ceil(cols / 128)][lds], one byte
+    each, in format "e4m3" or "e5m2"; keeps the tensors alive."""
+    for t in (q, scale):
+        if t.dim() != 2 or t.element_size() != 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise S2RError(S2R_ERR_DIM, "q8_mat")
+    if fmt not in _FORMATS:
+        raise S2RError(S2R_ERR_DIM, "q8_mat")
+    ld, lds = (max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0) for t in (q, scale))
+    m = s2r_q8_mat(q.data_ptr(), ld, scale.data_ptr(), lds, _FORMATS[fmt])
+    m.codes, m.scales = q, scale
+    return m
+
+
+def alloc_q8(rows: int, cols: int, fmt: str = "e4m3", square: bool = False,
+             device="cuda") -> s2r_q8_mat:
+    """An 8-bit matrix on new tensors (.codes, .scales), row blocks or with `square` 128 x 128
+    blocks, padded as the calls need it."""
+    import torch
+    up = lambda n, m: -(-n // m) * m
+    sr = up(rows, 128) // 128 if square else rows
+    return q8_mat(torch.empty((rows, up(max(cols, 1), 16)), dtype=torch.uint8, device=device),
+                  torch.empty((up(cols, 128) // 128, up(max(sr, 1), 4)), dtype=torch.uint8,
+                              device=device), fmt)
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def _ws(workspace, ws_bytes):
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _ptr(workspace), ws_bytes
+
+
+def _act(act) -> int:
+    return _ACTS.get(act, -1) if isinstance(act, str) else act
+
+
+def s2r_q8_save(M: int, K: int, x: s2r_mat, out: s2r_q8_mat, stream=None) -> None:
+    """x [M][K] to 8 bits, one scale per 128 elements of a row."""
+    _check(lib().s2r_q8_save(M, K, _ref(x), _ref(out), _stream(stream)), "s2r_q8_save")
+
+
+def s2r_q8_load(M: int, K: int, q: s2r_q8_mat, x: s2r_mat, stream=None) -> None:
+    """The stored values of q [M][K] into x."""
+    _check(lib().s2r_q8_load(M, K, _ref(q), _ref(x), _stream(stream)), "s2r_q8_load")
+
+
+def s2r_q8_weight(N: int, K: int, w: s2r_mat, out: s2r_q8_mat, out_t: s2r_q8_mat | None = None,
+                  stream=None) -> None:
+    """w [N][K] to 8 bits, one scale per 128 x 128 block, and its transpose into out_t."""
+    _check(lib().s2r_q8_weight(N, K, _ref(w), _ref(out), _ref(out_t), _stream(stream)),
+           "s2r_q8_weight")
+
+
+def s2r_q8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().s2r_q8_gemm_workspace_bytes(M, N, K))
+
+
+def s2r_q8_gemm(M: int, N: int, K: int, a: s2r_q8_mat, b: s2r_q8_mat, c: s2r_mat, workspace=None,
+                ws_bytes: int | None = None, stream=None) -> None:
+    """c [M][N] = a [M][K] b [N][K]^T (a in row blocks, b in square blocks)."""
+    ws, nb = _ws(workspace, ws_bytes)
+    _check(lib().s2r_q8_gemm(M, N, K, _ref(a), _ref(b), _ref(c), ws, nb, _stream(stream)),
+           "s2r_q8_gemm")
+
+
+def s2r_q8_wgrad_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().s2r_q8_wgrad_workspace_bytes(M, N, K))
+
+
+def s2r_q8_wgrad(M: int, N: int, K: int, dy, x: s2r_q8_mat, dw, lddw: int,
+                 accumulate: bool = False, workspace=None, ws_bytes: int | None = None,
+                 stream=None) -> None:
+    """dw [N][lddw] (+)= dy^T x, dy a bf16 s2r_mat or an s2r_q8_mat; dw fp32, a tensor or an
+    address within a worker's gradient row."""
+    ws, nb = _ws(workspace, ws_bytes)
+    wide = isinstance(dy, s2r_mat)
+    _check(lib().s2r_q8_wgrad(M, N, K, _ref(dy) if wide else None, None if wide else _ref(dy),
+                              _ref(x), _ptr(dw), lddw, 1 if accumulate else 0, ws, nb,
+                              _stream(stream)), "s2r_q8_wgrad")
+
+
+def s2r_q8_glu(M: int, F: int, act, g: s2r_mat, u: s2r_mat | None = None,
+               gq: s2r_q8_mat | None = None, uq: s2r_q8_mat | None = None,
+               y: s2r_mat | None = None, yq: s2r_q8_mat | None = None, stream=None) -> None:
+    """act(g) * u, or act(g) without u; act is "silu", "gelu" or "gelu_tanh"."""
+    _check(lib().s2r_q8_glu(M, F, _act(act), _ref(g), _ref(u), _ref(gq), _ref(uq), _ref(y),
+                            _ref(yq), _stream(stream)), "s2r_q8_glu")
+
+
+def s2r_q8_glu_grad(M: int, F: int, act, gq: s2r_q8_mat, uq: s2r_q8_mat | None, dy: s2r_mat,
+                    dg: s2r_mat | None = None, du: s2r_mat | None = None,
+                    dgq: s2r_q8_mat | None = None, duq: s2r_q8_mat | None = None,
+                    stream=None) -> None:
+    """The gradients of s2r_q8_glu's g and u from their checkpoints."""
+    _check(lib().s2r_q8_glu_grad(M, F, _act(act), _ref(gq), _ref(uq), _ref(dy), _ref(dg), _ref(du),
+                                 _ref(dgq), _ref(duq), _stream(stream)), "s2r_q8_glu_grad")
+
+
 TRACE_MAX = 64
 
 
@@ -321,6 +475,9 @@ __all__ = [
     "s2r_block_bitmap_words",
     "s2r_encode_workspace_bytes", "s2r_encode", "s2r_encode_noalloc", "s2r_reduce", "s2r_decode_workspace_bytes",
     "s2r_decode", "s2r_hash", "s2r_gather_sum", "s2r_topk_workspace_bytes", "s2r_topk_ef",
+    "s2r_mat", "s2r_q8_mat", "mat", "q8_mat", "alloc_q8", "s2r_q8_save", "s2r_q8_load",
+    "s2r_q8_weight", "s2r_q8_gemm_workspace_bytes", "s2r_q8_gemm",
+    "s2r_q8_wgrad_workspace_bytes", "s2r_q8_wgrad", "s2r_q8_glu", "s2r_q8_glu_grad",
     "s2r_trace", "s2r_diag_trace_attach",
     "alloc_encode_buffers", "status_string", "lib",
 ]

@@ -1,0 +1,250 @@
+// q8_glu.hip -- the activation of a feed-forward layer with 8-bit checkpoints, and its
+// gradient from them: s2r_q8_glu, s2r_q8_glu_grad.
+//
+//   forward   y = act(g) u;  g, u and y leave in 8 bits (and y in 16 or 32 if asked)
+//   backward  dg = dy u act'(g), du = dy act(g), with g and u as stored
+// act and act' share their transcendental:
+//   SiLU       s = 1 / (1 + e^-g):            act = g s,  act' = s (1 + g (1 - s))
+//   GELU       c = (1 + erf(g / sqrt 2)) / 2: act = g c,  act' = c + g e^(-g^2 / 2) / sqrt(2 pi)
+//   GELU_TANH  s = 1 / (1 + e^(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3), which is
+//              (1 + tanh z) / 2:              act = g s,  act' = s + g s (1 - s) 2 z'
+// Element-wise apart from the blocks' largest magnitudes: one read and one write of
+// everything, bound by HBM.
+#include "q8_device.hpp"
+#include "q8_launch.hpp"
+
+namespace s2r {
+
+constexpr int kGluThreads = 256;
+constexpr int kGluRows = kGluThreads / 8;
+constexpr int kGluBlocks = 2;  // blocks of 128 columns per workgroup: two or three streams each
+
+__device__ inline float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+template <int ACT>
+__device__ inline float act_value(float g) {
+  if (ACT == S2R_ACT_SILU) return g * sigmoid(g);
+  if (ACT == S2R_ACT_GELU) return g * (0.5f + 0.5f * erff(g * 0.70710678118654752f));
+  const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+  return g * sigmoid(z2);
+}
+
+template <int ACT>
+__device__ inline void act_both(float g, float& a, float& d) {
+  if (ACT == S2R_ACT_SILU) {
+    const float s = sigmoid(g);
+    a = g * s;
+    d = s * (1.0f + g * (1.0f - s));
+  } else if (ACT == S2R_ACT_GELU) {
+    const float c = 0.5f + 0.5f * erff(g * 0.70710678118654752f);
+    a = g * c;
+    d = c + g * (expf(-0.5f * g * g) * 0.39894228040143268f);
+  } else {
+    const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    const float s = sigmoid(z2);
+    a = g * s;
+    d = s + a * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * g * g));
+  }
+}
+
+// Where 16 columns of one row go: in 8 bits, their block's scale over 8 lanes, ...
+__device__ inline void put8(const s2r_q8_mat& o, uint32_t m, uint32_t c, uint32_t F,
+                            const float (&v)[16]) {
+  const uint32_t am = max_over_8(amax16(v));
+  uint32_t sb;
+  u32x4 code;
+  if (o.format == S2R_E4M3) {
+    sb = scale_byte<S2R_E4M3>(am);
+    code = encode16<S2R_E4M3>(v, scale_inverse(sb));
+  } else {
+    sb = scale_byte<S2R_E5M2>(am);
+    code = encode16<S2R_E5M2>(v, scale_inverse(sb));
+  }
+  if (c >= F) return;
+  store_codes16(o.q + (uint64_t)m * o.ld, c, F, code);
+  if (threadIdx.x % 8 == 0) o.scale[(uint64_t)(c / kQ8Block) * o.lds + m] = (uint8_t)sb;
+}
+
+// ... or in 16 or 32.
+__device__ inline void put(const s2r_mat& o, uint32_t m, uint32_t c, uint32_t F,
+                           const float (&v)[16]) {
+  if (c >= F) return;
+  if (o.dtype == S2R_BF16)
+    store16<S2R_BF16>(static_cast<uint16_t*>(o.data) + (uint64_t)m * o.ld, c, F, v);
+  else if (o.dtype == S2R_F16)
+    store16<S2R_F16>(static_cast<uint16_t*>(o.data) + (uint64_t)m * o.ld, c, F, v);
+  else
+    store16<S2R_F32>(static_cast<uint32_t*>(o.data) + (uint64_t)m * o.ld, c, F, v);
+}
+
+// Outputs that the caller left out have a null pointer.
+template <int DT, int ACT, bool GATED>
+__global__ __launch_bounds__(kGluThreads) void k_q8_glu(
+    const void* __restrict__ g, uint64_t ldg, const void* __restrict__ u, uint64_t ldu,
+    s2r_q8_mat gq, s2r_q8_mat uq, s2r_mat y, s2r_q8_mat yq, uint32_t M, uint32_t F,
+    uint32_t col_tiles) {
+  using E = typename ElemT<DT>::type;
+  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t m = rt * kGluRows + threadIdx.x / 8;
+  if (m >= M) return;  // whole groups of 8 lanes leave together
+  const uint32_t c0 = ct * (kGluBlocks * kQ8Block) + (threadIdx.x % 8) * 16;
+  const E* grow = static_cast<const E*>(g) + (uint64_t)m * ldg;
+  const E* urow = GATED ? static_cast<const E*>(u) + (uint64_t)m * ldu : nullptr;
+  Raw16<DT> rg[kGluBlocks], ru[GATED ? kGluBlocks : 1];
+#pragma unroll
+  for (int b = 0; b < kGluBlocks; ++b) {
+    rg[b] = load_raw16<DT>(grow, c0 + b * kQ8Block, F);
+    if (GATED) ru[b] = load_raw16<DT>(urow, c0 + b * kQ8Block, F);
+  }
+#pragma unroll
+  for (int b = 0; b < kGluBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    float v[16], w[16];
+    unpack16<DT>(rg[b], v);
+    if (gq.q) put8(gq, m, c, F, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+    if (GATED) {
+      unpack16<DT>(ru[b], w);
+      if (uq.q) put8(uq, m, c, F, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= w[i];
+    }
+    if (y.data) put(y, m, c, F, v);
+    if (yq.q) put8(yq, m, c, F, v);
+  }
+}
+
+template <int FMT, int ACT, bool GATED>
+__global__ __launch_bounds__(kGluThreads) void k_q8_glu_grad(
+    s2r_q8_mat gq, s2r_q8_mat uq, s2r_mat dy, s2r_mat dg, s2r_mat du, s2r_q8_mat dgq,
+    s2r_q8_mat duq, uint32_t M, uint32_t F, uint32_t col_tiles) {
+  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t m = rt * kGluRows + threadIdx.x / 8;
+  if (m >= M) return;
+  const uint32_t c0 = ct * (kGluBlocks * kQ8Block) + (threadIdx.x % 8) * 16;
+  u32x4 cg[kGluBlocks], cu[GATED ? kGluBlocks : 1];
+  uint32_t sg[kGluBlocks], su[GATED ? kGluBlocks : 1];
+  Raw16<S2R_BF16> r16[kGluBlocks];
+  Raw16<S2R_F32> r32[kGluBlocks];
+  const bool wide = dy.dtype == S2R_F32;
+#pragma unroll
+  for (int b = 0; b < kGluBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    const uint64_t sat = (uint64_t)(c / kQ8Block);
+    cg[b] = load_codes16(gq.q + (uint64_t)m * gq.ld, c, F);
+    sg[b] = c < F ? gq.scale[sat * gq.lds + m] : 127;
+    if (GATED) {
+      cu[b] = load_codes16(uq.q + (uint64_t)m * uq.ld, c, F);
+      su[b] = c < F ? uq.scale[sat * uq.lds + m] : 127;
+    }
+    if (wide)
+      r32[b] = load_raw16<S2R_F32>(static_cast<const uint32_t*>(dy.data) + (uint64_t)m * dy.ld, c, F);
+    else
+      r16[b] = load_raw16<S2R_BF16>(static_cast<const uint16_t*>(dy.data) + (uint64_t)m * dy.ld, c, F);
+  }
+#pragma unroll
+  for (int b = 0; b < kGluBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    float t[16], vg[16], vu[16];
+    if (wide) {
+      unpack16<S2R_F32>(r32[b], t);
+    } else if (dy.dtype == S2R_BF16) {
+      unpack16<S2R_BF16>(r16[b], t);
+    } else {
+      unpack16<S2R_F16>(__builtin_bit_cast(Raw16<S2R_F16>, r16[b]), t);
+    }
+    decode16<FMT>(cg[b], scale_value(sg[b]), vg);
+    if (GATED) decode16<FMT>(cu[b], scale_value(su[b]), vu);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a, d;
+      act_both<ACT>(vg[i], a, d);
+      if (GATED) {
+        vg[i] = t[i] * vu[i] * d;
+        vu[i] = t[i] * a;
+      } else {
+        vg[i] = t[i] * d;
+      }
+    }
+    if (dg.data) put(dg, m, c, F, vg);
+    if (dgq.q) put8(dgq, m, c, F, vg);
+    if (GATED) {
+      if (du.data) put(du, m, c, F, vu);
+      if (duq.q) put8(duq, m, c, F, vu);
+    }
+  }
+}
+
+namespace {
+
+template <int DT, int ACT>
+void go_glu(uint32_t grid, hipStream_t s, uint64_t M, uint64_t F, uint32_t ct, const s2r_mat& g,
+            const s2r_mat* u, const s2r_q8_mat& gq, const s2r_q8_mat& uq, const s2r_mat& y,
+            const s2r_q8_mat& yq) {
+  if (u)
+    hipLaunchKernelGGL((k_q8_glu<DT, ACT, true>), dim3(grid), dim3(kGluThreads), 0, s, g.data, g.ld,
+                       u->data, u->ld, gq, uq, y, yq, (uint32_t)M, (uint32_t)F, ct);
+  else
+    hipLaunchKernelGGL((k_q8_glu<DT, ACT, false>), dim3(grid), dim3(kGluThreads), 0, s, g.data,
+                       g.ld, nullptr, 0, gq, uq, y, yq, (uint32_t)M, (uint32_t)F, ct);
+}
+
+template <int FMT, int ACT>
+void go_grad(uint32_t grid, hipStream_t s, uint64_t M, uint64_t F, uint32_t ct,
+             const s2r_q8_mat& gq, const s2r_q8_mat* uq, const s2r_mat& dy, const s2r_mat& dg,
+             const s2r_mat& du, const s2r_q8_mat& dgq, const s2r_q8_mat& duq) {
+  if (uq)
+    hipLaunchKernelGGL((k_q8_glu_grad<FMT, ACT, true>), dim3(grid), dim3(kGluThreads), 0, s, gq, *uq,
+                       dy, dg, du, dgq, duq, (uint32_t)M, (uint32_t)F, ct);
+  else
+    hipLaunchKernelGGL((k_q8_glu_grad<FMT, ACT, false>), dim3(grid), dim3(kGluThreads), 0, s, gq,
+                       s2r_q8_mat{}, dy, dg, du, dgq, duq, (uint32_t)M, (uint32_t)F, ct);
+}
+
+#define S2R_Q8_ACT(act, CALL)                                              \
+  do {                                                                     \
+    if ((act) == S2R_ACT_SILU) { constexpr int ACT = S2R_ACT_SILU; CALL; } \
+    else if ((act) == S2R_ACT_GELU) { constexpr int ACT = S2R_ACT_GELU; CALL; } \
+    else { constexpr int ACT = S2R_ACT_GELU_TANH; CALL; }                  \
+  } while (0)
+
+inline s2r_q8_mat or_none(const s2r_q8_mat* m) { return m ? *m : s2r_q8_mat{}; }
+inline s2r_mat or_none(const s2r_mat* m) { return m ? *m : s2r_mat{}; }
+
+}  // namespace
+
+hipError_t launch_q8_glu(uint64_t M, uint64_t F, s2r_act act, const s2r_mat& g, const s2r_mat* u,
+                         const s2r_q8_mat* gq, const s2r_q8_mat* uq, const s2r_mat* y,
+                         const s2r_q8_mat* yq, hipStream_t s) {
+  const uint32_t ct = (uint32_t)((F + kGluBlocks * kQ8Block - 1) / (kGluBlocks * kQ8Block));
+  const uint32_t grid = (uint32_t)((M + kGluRows - 1) / kGluRows * ct);
+  const s2r_q8_mat a = or_none(gq), b = or_none(uq), c = or_none(yq);
+  const s2r_mat d = or_none(y);
+  trace_mark(s, "k_q8_glu");
+  if (g.dtype == S2R_BF16)
+    S2R_Q8_ACT(act, (go_glu<S2R_BF16, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
+  else if (g.dtype == S2R_F16)
+    S2R_Q8_ACT(act, (go_glu<S2R_F16, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
+  else
+    S2R_Q8_ACT(act, (go_glu<S2R_F32, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_glu_grad(uint64_t M, uint64_t F, s2r_act act, const s2r_q8_mat& gq,
+                              const s2r_q8_mat* uq, const s2r_mat& dy, const s2r_mat* dg,
+                              const s2r_mat* du, const s2r_q8_mat* dgq, const s2r_q8_mat* duq,
+                              hipStream_t s) {
+  const uint32_t ct = (uint32_t)((F + kGluBlocks * kQ8Block - 1) / (kGluBlocks * kQ8Block));
+  const uint32_t grid = (uint32_t)((M + kGluRows - 1) / kGluRows * ct);
+  const s2r_mat a = or_none(dg), b = or_none(du);
+  const s2r_q8_mat c = or_none(dgq), d = or_none(duq);
+  trace_mark(s, "k_q8_glu_grad");
+  if (gq.format == S2R_E4M3)
+    S2R_Q8_ACT(act, (go_grad<S2R_E4M3, ACT>(grid, s, M, F, ct, gq, uq, dy, a, b, c, d)));
+  else
+    S2R_Q8_ACT(act, (go_grad<S2R_E5M2, ACT>(grid, s, M, F, ct, gq, uq, dy, a, b, c, d)));
+  return hipGetLastError();
+}
+
+}  // namespace s2r

@@ -1,0 +1,206 @@
+// q8_store.hip -- matrices to 8 bits and back: s2r_q8_save, s2r_q8_load, s2r_q8_weight.
+//
+// For each block of 128 (a row's 128 elements, or 128 x 128): a = the largest finite
+// magnitude, scale = the least power of two with a <= MAX * scale, code = value / scale to
+// nearest even.  One read and one write of everything: bound by HBM.
+#include "q8_device.hpp"
+#include "q8_launch.hpp"
+
+namespace s2r {
+
+constexpr int kStoreThreads = 256;
+constexpr int kStoreRows = kStoreThreads / 8;  // rows of a workgroup's tile: 8 lanes per block
+constexpr int kStoreBlocks = 4;                // blocks of 128 columns of its tile
+
+// Lanes 8 j .. 8 j + 7 of a wave hold one row's block, 16 elements each; the 8 rows of a wave
+// are consecutive, so that their scale bytes are.
+template <int DT, int FMT>
+__global__ __launch_bounds__(kStoreThreads) void k_q8_save(
+    const void* __restrict__ x, uint64_t ldx, uint8_t* __restrict__ q, uint64_t ldq,
+    uint8_t* __restrict__ scale, uint64_t lds, uint32_t M, uint32_t K, uint32_t col_tiles) {
+  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t m = rt * kStoreRows + threadIdx.x / 8;
+  if (m >= M) return;  // whole groups of 8 lanes leave together
+  const uint32_t c0 = ct * (kStoreBlocks * kQ8Block) + (threadIdx.x % 8) * 16;
+  const auto* row = static_cast<const typename ElemT<DT>::type*>(x) + (uint64_t)m * ldx;
+  uint8_t* qrow = q + (uint64_t)m * ldq;
+  Raw16<DT> r[kStoreBlocks];
+#pragma unroll
+  for (int b = 0; b < kStoreBlocks; ++b) r[b] = load_raw16<DT>(row, c0 + b * kQ8Block, K);
+#pragma unroll
+  for (int b = 0; b < kStoreBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    float v[16];
+    unpack16<DT>(r[b], v);
+    const uint32_t sb = scale_byte<FMT>(max_over_8(amax16(v)));
+    if (c < K) store_codes16(qrow, c, K, encode16<FMT>(v, scale_inverse(sb)));
+    if (threadIdx.x % 8 == 0 && c < K) scale[(uint64_t)(c / kQ8Block) * lds + m] = (uint8_t)sb;
+  }
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kStoreThreads) void k_q8_load(
+    const uint8_t* __restrict__ q, uint64_t ldq, const uint8_t* __restrict__ scale, uint64_t lds,
+    void* __restrict__ x, uint64_t ldx, uint32_t M, uint32_t K, uint32_t col_tiles) {
+  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t m = rt * kStoreRows + threadIdx.x / 8;
+  if (m >= M) return;
+  const uint32_t c0 = ct * (kStoreBlocks * kQ8Block) + (threadIdx.x % 8) * 16;
+  const uint8_t* qrow = q + (uint64_t)m * ldq;
+  auto* row = static_cast<typename ElemT<DT>::type*>(x) + (uint64_t)m * ldx;
+  u32x4 r[kStoreBlocks];
+  uint32_t sb[kStoreBlocks];
+#pragma unroll
+  for (int b = 0; b < kStoreBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    r[b] = load_codes16(qrow, c, K);
+    sb[b] = c < K ? scale[(uint64_t)(c / kQ8Block) * lds + m] : 127;
+  }
+#pragma unroll
+  for (int b = 0; b < kStoreBlocks; ++b) {
+    const uint32_t c = c0 + b * kQ8Block;
+    float v[16];
+    decode16<FMT>(r[b], scale_value(sb[b]), v);
+    if (c < K) store16<DT>(row, c, K, v);
+  }
+}
+
+// One workgroup per 128 x 128 block: row t / 8 + 32 i of the block, 16 elements per lane.  The
+// transposed codes go through LDS, where each lane takes 16 rows x 4 columns as dwords and
+// transposes them 4 x 4 bytes at a time.
+constexpr int kWtStride = kQ8Block + 4;  // bytes of an LDS row: dword columns on distinct banks
+
+__device__ inline void transpose4(const uint32_t (&a)[4], uint32_t (&t)[4]) {
+  const uint32_t p = __builtin_amdgcn_perm(a[1], a[0], 0x05010400);  // a0.0 a1.0 a0.1 a1.1
+  const uint32_t q = __builtin_amdgcn_perm(a[1], a[0], 0x07030602);  // a0.2 a1.2 a0.3 a1.3
+  const uint32_t r = __builtin_amdgcn_perm(a[3], a[2], 0x05010400);
+  const uint32_t s = __builtin_amdgcn_perm(a[3], a[2], 0x07030602);
+  t[0] = __builtin_amdgcn_perm(r, p, 0x05040100);
+  t[1] = __builtin_amdgcn_perm(r, p, 0x07060302);
+  t[2] = __builtin_amdgcn_perm(s, q, 0x05040100);
+  t[3] = __builtin_amdgcn_perm(s, q, 0x07060302);
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kStoreThreads) void k_q8_weight(
+    const void* __restrict__ w, uint64_t ldw, uint8_t* __restrict__ q, uint64_t ldq,
+    uint8_t* __restrict__ scale, uint64_t lds, uint8_t* __restrict__ qt, uint64_t ldt,
+    uint8_t* __restrict__ scale_t, uint64_t ldst, uint32_t N, uint32_t K, uint32_t col_blocks) {
+  __shared__ uint32_t wave_max[kStoreThreads / 64];
+  __shared__ uint32_t tile[kQ8Block * kWtStride / 4];
+  const uint32_t kb = blockIdx.x % col_blocks, nb = blockIdx.x / col_blocks;
+  const uint32_t t = threadIdx.x;
+  const uint32_t c = kb * kQ8Block + (t % 8) * 16;
+  Raw16<DT> r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = nb * kQ8Block + t / 8 + 32 * i;
+    const auto* row = static_cast<const typename ElemT<DT>::type*>(w) + (uint64_t)n * ldw;
+    r[i] = load_raw16<DT>(row, c, n < N ? K : 0);
+  }
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[16];
+    unpack16<DT>(r[i], v);
+    am = umax(am, amax16(v));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) am = umax(am, (uint32_t)__shfl_xor((int)am, o));
+  if (t % 64 == 0) wave_max[t / 64] = am;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kStoreThreads / 64; ++i) am = umax(am, wave_max[i]);
+  const uint32_t sb = scale_byte<FMT>(am);
+  if (t == 0) {
+    scale[(uint64_t)kb * lds + nb] = (uint8_t)sb;
+    if (qt) scale_t[(uint64_t)nb * ldst + kb] = (uint8_t)sb;
+  }
+  const float inv = scale_inverse(sb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t rr = t / 8 + 32 * i, n = nb * kQ8Block + rr;
+    float v[16];
+    unpack16<DT>(r[i], v);
+    const u32x4 code = encode16<FMT>(v, inv);
+    if (n < N && c < K) store_codes16(q + (uint64_t)n * ldq, c, K, code);
+    if (qt) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tile[(rr * kWtStride + (t % 8) * 16) / 4 + j] = code[j];
+    }
+  }
+  if (!qt) return;
+  __syncthreads();
+  const uint32_t ng = t % 8, kg = t / 8;  // 16 rows n, 4 columns k
+  u32x4 out[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    uint32_t in[4], tr[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) in[j] = tile[(ng * 16 + a * 4 + j) * (kWtStride / 4) + kg];
+    transpose4(in, tr);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j][a] = tr[j];
+  }
+  const uint32_t n0 = nb * kQ8Block + ng * 16;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t k = kb * kQ8Block + kg * 4 + j;
+    if (k < K && n0 < N) store_codes16(qt + (uint64_t)k * ldt, n0, N, out[j]);
+  }
+}
+
+#define S2R_Q8_DISPATCH(dtype, format, CALL)                                       \
+  do {                                                                             \
+    if ((format) == S2R_E4M3) {                                                    \
+      constexpr int FMT = S2R_E4M3;                                                \
+      if ((dtype) == S2R_BF16) { constexpr int DT = S2R_BF16; CALL; }              \
+      else if ((dtype) == S2R_F16) { constexpr int DT = S2R_F16; CALL; }           \
+      else { constexpr int DT = S2R_F32; CALL; }                                   \
+    } else {                                                                       \
+      constexpr int FMT = S2R_E5M2;                                                \
+      if ((dtype) == S2R_BF16) { constexpr int DT = S2R_BF16; CALL; }              \
+      else if ((dtype) == S2R_F16) { constexpr int DT = S2R_F16; CALL; }           \
+      else { constexpr int DT = S2R_F32; CALL; }                                   \
+    }                                                                              \
+  } while (0)
+
+hipError_t launch_q8_save(uint64_t M, uint64_t K, const s2r_mat& x, const s2r_q8_mat& out,
+                          hipStream_t s) {
+  const uint64_t ct = (K + kStoreBlocks * kQ8Block - 1) / (kStoreBlocks * kQ8Block);
+  const uint64_t rt = (M + kStoreRows - 1) / kStoreRows;
+  trace_mark(s, "k_q8_save");
+  S2R_Q8_DISPATCH(x.dtype, out.format,
+                  hipLaunchKernelGGL((k_q8_save<DT, FMT>), dim3((uint32_t)(ct * rt)),
+                                     dim3(kStoreThreads), 0, s, x.data, x.ld, out.q, out.ld,
+                                     out.scale, out.lds, (uint32_t)M, (uint32_t)K, (uint32_t)ct));
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_load(uint64_t M, uint64_t K, const s2r_q8_mat& in, const s2r_mat& x,
+                          hipStream_t s) {
+  const uint64_t ct = (K + kStoreBlocks * kQ8Block - 1) / (kStoreBlocks * kQ8Block);
+  const uint64_t rt = (M + kStoreRows - 1) / kStoreRows;
+  trace_mark(s, "k_q8_load");
+  S2R_Q8_DISPATCH(x.dtype, in.format,
+                  hipLaunchKernelGGL((k_q8_load<DT, FMT>), dim3((uint32_t)(ct * rt)),
+                                     dim3(kStoreThreads), 0, s, in.q, in.ld, in.scale, in.lds,
+                                     x.data, x.ld, (uint32_t)M, (uint32_t)K, (uint32_t)ct));
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_weight(uint64_t N, uint64_t K, const s2r_mat& w, const s2r_q8_mat& out,
+                            const s2r_q8_mat* out_t, hipStream_t s) {
+  const uint64_t kb = (K + kQ8Block - 1) / kQ8Block, nb = (N + kQ8Block - 1) / kQ8Block;
+  trace_mark(s, "k_q8_weight");
+  S2R_Q8_DISPATCH(w.dtype, out.format,
+                  hipLaunchKernelGGL((k_q8_weight<DT, FMT>), dim3((uint32_t)(kb * nb)),
+                                     dim3(kStoreThreads), 0, s, w.data, w.ld, out.q, out.ld,
+                                     out.scale, out.lds, out_t ? out_t->q : nullptr,
+                                     out_t ? out_t->ld : 0, out_t ? out_t->scale : nullptr,
+                                     out_t ? out_t->lds : 0, (uint32_t)N, (uint32_t)K,
+                                     (uint32_t)kb));
+  return hipGetLastError();
+}
+
+}  // namespace s2r
