@@ -1,0 +1,55 @@
+// q8_tile.hpp -- what the two tiled products share: direct loads to LDS, barriers, the order
+// of tiles over the chip and the sum of partial results (internal to libs2r).
+#pragma once
+
+#include "q8_device.hpp"
+#include "s2r_device.hpp"
+
+namespace s2r {
+
+constexpr uint32_t kTileCus = 256;   // compute units of an MI355X
+constexpr uint32_t kTileGroup = 8;   // rows of tiles that are walked together
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// A bounds-checked view of global memory: reads at or beyond `bytes` give zeros.
+__device__ inline __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, uint64_t bytes) {
+  const uint32_t n = bytes > 0xffffffffull ? 0xffffffffu : (uint32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, (int)n, 0x00020000);
+}
+
+// 16 bytes per lane from `at` bytes into the view to LDS, lane i at `lds` + 16 i; `lds` is
+// the same for the wave.
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, at, 0, 0, 0);
+}
+
+// Every load of this wave has arrived and every LDS access is done, for all waves.
+__device__ inline void drain_and_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Workgroup b of `total` to a tile and a part of the sum.  Consecutive workgroups go to
+// the eight accelerator dies in turn, so the work list is cut into eight stretches, one for
+// each die and its L2; within a stretch kTileGroup rows of tiles are walked column by column,
+// so that the workgroups that run together on a die share rows and columns of both operands.
+struct TileAt {
+  uint32_t row, col, part;
+};
+__device__ inline TileAt tile_at(uint32_t b, uint32_t rows, uint32_t cols, uint32_t total) {
+  const uint32_t die = b % kXcds, per = total / kXcds, rem = total % kXcds;
+  uint32_t lin = die * per + min(die, rem) + b / kXcds;
+  TileAt t;
+  t.part = lin / (rows * cols);
+  lin -= t.part * (rows * cols);
+  const uint32_t span = kTileGroup * cols, g = lin / span, first = g * kTileGroup;
+  const uint32_t height = min(rows - first, kTileGroup), in = lin - g * span;
+  t.row = first + in % height;
+  t.col = in / height;
+  return t;
+}
+
+}  // namespace s2r
