@@ -129,6 +129,27 @@ __device__ inline void store16(void* row, uint32_t col, uint32_t cols, const flo
   }
 }
 
+// Four fp32 values to columns c .. c + 3 of row m, c a multiple of 4; those at or beyond `cols`
+// are left alone.
+__device__ inline void store4(const s2r_mat& o, uint32_t m, uint32_t c, uint32_t cols, f32x4 v) {
+  const uint64_t at = (uint64_t)m * o.ld + c;
+  if (o.dtype == S2R_F32) {
+    float* p = static_cast<float*>(o.data) + at;
+    if (c + 4 <= cols) *reinterpret_cast<f32x4*>(p) = v;
+    else
+      for (uint32_t e = 0; c + e < cols; ++e) p[e] = e == 0 ? v[0] : e == 1 ? v[1] : v[2];
+    return;
+  }
+  const bool bf = o.dtype == S2R_BF16;
+  const u32x2 h = {bf ? pack2<S2R_BF16>(v[0], v[1]) : pack2<S2R_F16>(v[0], v[1]),
+                   bf ? pack2<S2R_BF16>(v[2], v[3]) : pack2<S2R_F16>(v[2], v[3])};
+  uint16_t* p = static_cast<uint16_t*>(o.data) + at;
+  if (c + 4 <= cols) *reinterpret_cast<u32x2*>(p) = h;
+  else
+    for (uint32_t e = 0; c + e < cols; ++e)
+      p[e] = (uint16_t)(e == 0 ? h[0] : e == 1 ? h[0] >> 16 : h[1]);
+}
+
 // ---- the scale ----------------------------------------------------------------------------
 template <int FMT>
 constexpr int scale_bias() { return FMT == S2R_E4M3 ? 8 : 15; }

@@ -41,7 +41,7 @@ __device__ inline f32x4 mma(const i32x8& b, const i32x8& a, const f32x4& c, uint
 // WM x WN waves, each 64 IM rows of A by 64 rows of B; a step is one block of 128 of the sum.
 // LDS holds 128 bytes of every row of both operands, twice: one half is filled directly from
 // global memory while the other is multiplied.  16-byte piece s of LDS row p lies at
-// s ^ (p % 8), which spreads the 16 rows of a fragment over the banks.
+// s ^ (p / 2 % 8): the 16 lanes that read together, one piece of 16 rows, meet every bank once.
 // Rows of A are taken in the order m = 64 I + 4 r + i (fragment i of group I, lane r), so the
 // scales of a lane's four fragments are one dword; rows of B in the order
 // n = 16 g + 4 j + t (fragment j, row 4 g + t), so a lane's results are 16 consecutive columns.
@@ -65,18 +65,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_q8_gemm(s2r_q8_mat a, s2r_q8_m
 
   // where this lane's pieces of a step come from, relative to the tile's first row
   uint32_t from_a[kLoadsA], from_b[kLoadsB];
-  const uint32_t piece = (lane % 8 ^ lane / 8) * 16;
 #pragma unroll
   for (int j = 0; j < kLoadsA; ++j) {
     const uint32_t p = (wave * kLoadsA + j) * 8 + lane / 8;
     const uint32_t row = p / 64 * 64 + 4 * (p % 16) + p % 64 / 16;
-    from_a[j] = min(row, M - 1 - m0) * (uint32_t)a.ld + piece;
+    from_a[j] = min(row, M - 1 - m0) * (uint32_t)a.ld + (lane % 8 ^ p / 2 % 8) * 16;
   }
 #pragma unroll
   for (int j = 0; j < kLoadsB; ++j) {
     const uint32_t p = (wave * kLoadsB + j) * 8 + lane / 8;
     const uint32_t row = p / 64 * 64 + 16 * (p % 16 / 4) + 4 * (p % 64 / 16) + p % 4;
-    from_b[j] = min(row, N - 1 - n0) * (uint32_t)b.ld + piece;
+    from_b[j] = min(row, N - 1 - n0) * (uint32_t)b.ld + (lane % 8 ^ p / 2 % 8) * 16;
   }
   const uint64_t base_a = (uint64_t)a.q + (uint64_t)m0 * a.ld, len_a = (uint64_t)(M - m0) * a.ld;
   const uint64_t base_b = (uint64_t)b.q + (uint64_t)n0 * b.ld, len_b = (uint64_t)(N - n0) * b.ld;
@@ -104,8 +103,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_q8_gemm(s2r_q8_mat a, s2r_q8_m
   };
 
   f32x4 acc[4 * IM][4] = {};
-  const uint32_t lo = r * kQ8Block + (2 * g ^ r % 8) * 16;
-  const uint32_t hi = r * kQ8Block + ((2 * g + 1) ^ r % 8) * 16;
+  const uint32_t lo = r * kQ8Block + (2 * g ^ r / 2) * 16;
+  const uint32_t hi = r * kQ8Block + ((2 * g + 1) ^ r / 2) * 16;
   auto frag = [&](const uint8_t* p) {
     return join(*reinterpret_cast<const u32x4*>(p + lo), *reinterpret_cast<const u32x4*>(p + hi));
   };
@@ -129,7 +128,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_q8_gemm(s2r_q8_mat a, s2r_q8_m
   auto clear_tail = [&](uint8_t* lds) {
     const int left = (int)(K % kQ8Block);
     for (uint32_t e = threadIdx.x; e < (TM + TN) * 8; e += 64 * kWaves) {
-      const int keep = left - 16 * (int)(e % 8 ^ e / 8 % 8);
+      const int keep = left - 16 * (int)(e % 8 ^ e / 16 % 8);
       if (keep >= 16) continue;
       u32x4* at = reinterpret_cast<u32x4*>(lds + e * 16);
       u32x4 v = *at;
@@ -183,26 +182,105 @@ __global__ __launch_bounds__(64 * WM * WN) void k_q8_gemm(s2r_q8_mat a, s2r_q8_m
   }
 }
 
+// ---- few rows -----------------------------------------------------------------------------
+// Up to 16 FM rows of A: the rows of B are read once, straight into registers, and bound the
+// call.  A workgroup takes 16 of them and cuts the sum among its waves, block by block in
+// turn; the partial sums meet in LDS and are added in the order of the waves.
+constexpr int kFewBatch = 2;  // blocks of the sum a wave has in flight
+
+__device__ inline i32x8 load_frag(const uint8_t* row, uint32_t k, uint32_t K) {
+  return join(load_codes16(row, k, K), load_codes16(row, k + 16, K));
+}
+
+template <int FA, int FB, int FM, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8_mat b, s2r_mat c,
+                                                            uint32_t M, uint32_t N, uint32_t K) {
+  __shared__ f32x4 part[WAVES][FM][64];
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * FM);
+  const uint32_t n = min(n0 + r, N - 1);
+  const uint8_t* rows_a[FM];
+  uint32_t ms[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    ms[i] = min(m0 + 16 * i + r, M - 1);
+    rows_a[i] = a.q + (uint64_t)ms[i] * a.ld;
+  }
+  const uint8_t* row_b = b.q + (uint64_t)n * b.ld;
+  const uint8_t* scale_b = b.scale + n0 / kQ8Block;
+  f32x4 acc[FM] = {};
+  const uint32_t steps = (K + kQ8Block - 1) / kQ8Block;
+  for (uint32_t s = wave; s < steps; s += WAVES * kFewBatch) {
+    i32x8 fb[kFewBatch], fa[kFewBatch][FM];
+    uint32_t sb[kFewBatch], sa[kFewBatch][FM];
+#pragma unroll
+    for (int e = 0; e < kFewBatch; ++e) {
+      const uint32_t at = s + e * WAVES, k = at * kQ8Block + 32 * g;
+      if (at >= steps) continue;
+      fb[e] = load_frag(row_b, k, K);
+      sb[e] = scale_b[(uint64_t)at * b.lds];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        fa[e][i] = load_frag(rows_a[i], k, K);
+        sa[e][i] = a.scale[(uint64_t)at * a.lds + ms[i]];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kFewBatch; ++e) {
+      if (s + e * WAVES >= steps) continue;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[i] = mma<FA, FB>(fb[e], fa[e][i], acc[i], sb[e], sa[e][i], 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < FM * 64; e += 64 * WAVES) {
+    f32x4 v = part[0][e / 64][e % 64];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += part[w][e / 64][e % 64];
+    const uint32_t m = m0 + e / 64 * 16 + e % 16, at = n0 + e % 64 / 16 * 4;
+    if (m < M) store4(c, m, at, N, v);
+  }
+}
+
 size_t q8_gemm_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
+
+namespace {
+
+template <int FA, int FB>
+void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_q8_mat& b,
+             const s2r_mat& c, hipStream_t s) {
+  const uint32_t m = (uint32_t)M, n = (uint32_t)N, k = (uint32_t)K;
+  if (M <= 64) {
+    trace_mark(s, "k_q8_gemm_few");
+    const dim3 grid((n + 15) / 16);
+    if (M <= 16)
+      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 1, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
+    else if (M <= 32)
+      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 2, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
+    else
+      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 4, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
+    return;
+  }
+  trace_mark(s, "k_q8_gemm");
+  const uint32_t mt = (m + 255) / 256, nt = (n + 255) / 256, steps = (k + kQ8Block - 1) / kQ8Block;
+  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 4, 2>), dim3(mt * nt), dim3(512), 0, s, a, b, c, 0, m, n,
+                     k, mt, nt, steps);
+}
+
+}  // namespace
 
 hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a,
                           const s2r_q8_mat& b, const s2r_mat& c, void*, hipStream_t s) {
-  constexpr int TM = 256, TN = 256;
-  const uint64_t nt = (N + TN - 1) / TN, mt = (M + TM - 1) / TM;
-  const uint64_t steps = (K + kQ8Block - 1) / kQ8Block;
-  trace_mark(s, "k_q8_gemm");
-#define S2R_GEMM(FA, FB)                                                                    \
-  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 4, 2>), dim3((uint32_t)(nt * mt)), dim3(512), 0, s, \
-                     a, b, c, 0, (uint32_t)M, (uint32_t)N, (uint32_t)K, (uint32_t)mt,        \
-                     (uint32_t)nt, (uint32_t)steps)
   if (a.format == S2R_E4M3) {
-    if (b.format == S2R_E4M3) S2R_GEMM(S2R_E4M3, S2R_E4M3);
-    else S2R_GEMM(S2R_E4M3, S2R_E5M2);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E4M3, S2R_E4M3>(M, N, K, a, b, c, s);
+    else go_gemm<S2R_E4M3, S2R_E5M2>(M, N, K, a, b, c, s);
   } else {
-    if (b.format == S2R_E4M3) S2R_GEMM(S2R_E5M2, S2R_E4M3);
-    else S2R_GEMM(S2R_E5M2, S2R_E5M2);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, s);
+    else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, s);
   }
-#undef S2R_GEMM
   return hipGetLastError();
 }
 
