@@ -10,6 +10,7 @@
 namespace s2r {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -148,6 +149,24 @@ __device__ inline void store4(const s2r_mat& o, uint32_t m, uint32_t c, uint32_t
   else
     for (uint32_t e = 0; c + e < cols; ++e)
       p[e] = (uint16_t)(e == 0 ? h[0] : e == 1 ? h[0] >> 16 : h[1]);
+}
+
+// Eight values to columns c .. c + 7 of row m, c a multiple of 8.
+__device__ inline void store8(const s2r_mat& o, uint32_t m, uint32_t c, uint32_t cols, f32x4 lo,
+                              f32x4 hi) {
+  if (c + 8 <= cols && o.dtype != S2R_F32) {
+    const bool bf = o.dtype == S2R_BF16;
+    u32x4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float x = w < 2 ? lo[2 * w] : hi[2 * w - 4], y = w < 2 ? lo[2 * w + 1] : hi[2 * w - 3];
+      v[w] = bf ? pack2<S2R_BF16>(x, y) : pack2<S2R_F16>(x, y);
+    }
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(o.data) + (uint64_t)m * o.ld + c) = v;
+    return;
+  }
+  store4(o, m, c, cols, lo);
+  if (c + 4 < cols) store4(o, m, c + 4, cols, hi);
 }
 
 // ---- the scale ----------------------------------------------------------------------------

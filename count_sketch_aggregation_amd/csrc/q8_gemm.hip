@@ -9,8 +9,7 @@
 namespace s2r {
 
 // ---- fragments ----------------------------------------------------------------------------
-// The matrix instruction takes 16 rows x 128 bytes from each side: lane l holds row l % 16,
-// bytes 32 (l / 16) .. + 31.
+// `at` is the byte of `sa` that holds this fragment's scale.
 __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
   i32x8 v;
 #pragma unroll
@@ -21,165 +20,279 @@ __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
   return v;
 }
 
-// `at` is the byte of `sa` that holds this fragment's scale.
+__device__ inline void clear_from(i32x8& v, int left) {  // `left` bytes stay
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const int l = left - 4 * w;
+    v[w] = l <= 0 ? 0 : l < 4 ? v[w] & (int)((1u << (8 * l)) - 1) : v[w];
+  }
+}
+
 template <int FA, int FB>
-__device__ inline f32x4 mma(const i32x8& b, const i32x8& a, const f32x4& c, uint32_t sb,
-                            uint32_t sa, int at) {
+__device__ inline f32x16 mma32(const i32x8& b, const i32x8& a, const f32x16& c, uint32_t sb,
+                               uint32_t sa, int at) {
   switch (at) {
     case 0:
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 0, (int)sa);
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 0, (int)sa);
     case 1:
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 1, (int)sa);
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 1, (int)sa);
     case 2:
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 2, (int)sa);
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 2, (int)sa);
     default:
-      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 3, (int)sa);
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 3, (int)sa);
   }
 }
 
 // ---- tiles --------------------------------------------------------------------------------
-// WM x WN waves, each 64 IM rows of A by 64 rows of B; a step is one block of 128 of the sum.
-// LDS holds 128 bytes of every row of both operands, twice: one half is filled directly from
-// global memory while the other is multiplied.  16-byte piece s of LDS row p lies at
-// s ^ (p / 2 % 8): the 16 lanes that read together, one piece of 16 rows, meet every bank once.
-// Rows of A are taken in the order m = 64 I + 4 r + i (fragment i of group I, lane r), so the
-// scales of a lane's four fragments are one dword; rows of B in the order
-// n = 16 g + 4 j + t (fragment j, row 4 g + t), so a lane's results are 16 consecutive columns.
-template <int FA, int FB, int WM, int WN, int IM>
-__global__ __launch_bounds__(64 * WM * WN) void k_q8_gemm(s2r_q8_mat a, s2r_q8_mat b, s2r_mat c,
-                                                          uint64_t part_bytes, uint32_t M, uint32_t N,
-                                                          uint32_t K, uint32_t m_tiles,
-                                                          uint32_t n_tiles, uint32_t part_steps) {
-  constexpr int kWaves = WM * WN, TM = 64 * IM * WM, TN = 64 * WN;
-  constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves;
+// WM x WN waves, each 32 FM rows of A by 32 FN rows of B; a block is 128 of the sum, one scale
+// of every row.  LDS holds two blocks, 128 bytes of every row of both operands: one is
+// multiplied while the next arrives straight from global memory, a whole line of each row.
+// A block is multiplied in two halves of 64, and the fragments of a half are read into
+// registers while the half before is multiplied: its LDS is free again after the first half.
+// 16-byte piece s of LDS row p lies at s ^ spread(p): the lanes that read together meet every
+// bank once.  Rows of A are taken in the order m = FM r + i (fragment i, lane r), so that the
+// scales of a lane's fragments are one load.
+// A workgroup stays for several tiles, and the blocks of all of them are one stream: the next
+// tile's first blocks arrive while the last ones of this are multiplied and its results leave.
+__device__ inline uint32_t spread(uint32_t p) { return p / 2 % 4 | p / 16 % 2 << 2; }
+
+// 32 x 64 results from LDS: rows m0, m0 + step, ..., columns n0 .. n0 + 63; lane l takes eight
+// columns of rows l / 8 + 8 k.  They leave through a view that ends with row M - 1; lanes
+// without eight columns aim beyond its end.
+template <int DT>
+__device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[4][2], uint32_t m0, uint32_t step,
+                                  uint32_t M, uint32_t n0, uint32_t N) {
+  constexpr uint32_t size = elem_bytes<DT>(), kNowhere = 0xffff0000u;
+  const uint64_t first = (uint64_t)m0 * c.ld + n0, last = (uint64_t)(M - 1) * c.ld + N;
+  const auto view = rsrc_of((uint64_t)c.data + first * size, (last - first) * size);
+  const uint32_t lane = threadIdx.x % 64, n = lane % 8 * 8;
+  const uint32_t ld = step * (uint32_t)c.ld * size;
+  const uint32_t at = n0 + n < N ? lane / 8 * ld + n * size : kNowhere;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    const uint32_t to = n0 + n < N ? at + 8 * k * ld : kNowhere;
+    const f32x4 lo = v[k][0], hi = v[k][1];
+    if (DT == S2R_F32) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), view, to, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), view, to + 16, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(
+          u32x4{pack2<DT>(lo[0], lo[1]), pack2<DT>(lo[2], lo[3]), pack2<DT>(hi[0], hi[1]),
+                pack2<DT>(hi[2], hi[3])}, view, to, 0, 0);
+    }
+  }
+}
+
+__device__ inline void store_turned(const s2r_mat& c, const uint8_t* lds, uint32_t m0, uint32_t step,
+                                    uint32_t M, uint32_t n0, uint32_t N) {
+  if (m0 >= M || n0 >= N) return;
+  const uint32_t lane = threadIdx.x % 64, s = lane % 8 * 2;
+  f32x4 v[4][2];
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    const uint32_t row = lane / 8 + 8 * k, mix = row % 8 | row / 16 * 8;
+    v[k][0] = *reinterpret_cast<const f32x4*>(lds + row * 256 + (s ^ mix) * 16);
+    v[k][1] = *reinterpret_cast<const f32x4*>(lds + row * 256 + ((s + 1) ^ mix) * 16);
+  }
+  if (n0 + 64 > N && N % 8 != 0) {  // a lane may have fewer than eight columns
+#pragma unroll 1
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t m = m0 + step * (lane / 8 + 8 * k), n = n0 + lane % 8 * 8;
+      const f32x4 lo = k == 0 ? v[0][0] : k == 1 ? v[1][0] : k == 2 ? v[2][0] : v[3][0];
+      const f32x4 hi = k == 0 ? v[0][1] : k == 1 ? v[1][1] : k == 2 ? v[2][1] : v[3][1];
+      if (m < M && n < N) store8(c, m, n, N, lo, hi);
+    }
+  } else if (c.dtype == S2R_BF16) {
+    store_rows<S2R_BF16>(c, v, m0, step, M, n0, N);
+  } else if (c.dtype == S2R_F16) {
+    store_rows<S2R_F16>(c, v, m0, step, M, n0, N);
+  } else {
+    store_rows<S2R_F32>(c, v, m0, step, M, n0, N);
+  }
+}
+
+template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
+    s2r_q8_mat a, s2r_q8_mat b, s2r_mat c, uint64_t part_bytes, uint32_t M, uint32_t N, uint32_t K,
+    uint32_t m_tiles, uint32_t n_tiles, uint32_t total, uint32_t part_blocks) {
+  constexpr int kWaves = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
+  constexpr int kLoadsA = TM / 8 / kWaves, kLoads = (TM + TN) / 8 / kWaves;
   constexpr int kBytes = (TM + TN) * kQ8Block;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBytes];
+  constexpr int kTurn = 32 * 64 * 4;  // a wave's room for 32 x 64 results
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBytes + kWaves * kTurn];
 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
-  const TileAt t = tile_at(blockIdx.x, m_tiles, n_tiles, gridDim.x);
-  const uint32_t m0 = t.row * TM, n0 = t.col * TN;
-  const uint32_t wm = wave / WN * (64 * IM), wn = wave % WN * 64;
-  const uint32_t steps = (K + kQ8Block - 1) / kQ8Block;
-  const uint32_t s0 = t.part * part_steps, s1 = min(s0 + part_steps, steps);
+  const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
+  const uint32_t wm = wave / WN * (32 * FM), wn = wave % WN * (32 * FN);
+  const uint32_t blocks = (K + kQ8Block - 1) / kQ8Block;
 
-  // where this lane's pieces of a step come from, relative to the tile's first row
-  uint32_t from_a[kLoadsA], from_b[kLoadsB];
+  // where this lane's pieces of a block come from, relative to the tile's first row
+  uint32_t from[kLoads];
 #pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const uint32_t p = (wave * kLoadsA + j) * 8 + lane / 8;
-    const uint32_t row = p / 64 * 64 + 4 * (p % 16) + p % 64 / 16;
-    from_a[j] = min(row, M - 1 - m0) * (uint32_t)a.ld + (lane % 8 ^ p / 2 % 8) * 16;
-  }
-#pragma unroll
-  for (int j = 0; j < kLoadsB; ++j) {
-    const uint32_t p = (wave * kLoadsB + j) * 8 + lane / 8;
-    const uint32_t row = p / 64 * 64 + 16 * (p % 16 / 4) + 4 * (p % 64 / 16) + p % 4;
-    from_b[j] = min(row, N - 1 - n0) * (uint32_t)b.ld + (lane % 8 ^ p / 2 % 8) * 16;
-  }
-  const uint64_t base_a = (uint64_t)a.q + (uint64_t)m0 * a.ld, len_a = (uint64_t)(M - m0) * a.ld;
-  const uint64_t base_b = (uint64_t)b.q + (uint64_t)n0 * b.ld, len_b = (uint64_t)(N - n0) * b.ld;
-  const uint8_t* scale_a[IM];
-#pragma unroll
-  for (int I = 0; I < IM; ++I)
-    scale_a[I] = a.scale + min(m0 + wm + 64 * I + 4 * r, (uint32_t)a.lds - 4);
-  const uint8_t* scale_b = b.scale + min(n0 + wn, N - 1) / kQ8Block;
-
-  auto load = [&](uint8_t* lds, uint32_t step) {
-    const uint64_t k = (uint64_t)step * kQ8Block;
-    const auto ra = rsrc_of(base_a + k, len_a - k), rb = rsrc_of(base_b + k, len_b - k);
-#pragma unroll
-    for (int j = 0; j < kLoadsA; ++j)
-      load_to_lds(ra, lds + (wave * kLoadsA + j) * 1024, from_a[j]);
-#pragma unroll
-    for (int j = 0; j < kLoadsB; ++j)
-      load_to_lds(rb, lds + TM * kQ8Block + (wave * kLoadsB + j) * 1024, from_b[j]);
-  };
-  auto load_scales = [&](uint32_t (&sa)[IM], uint32_t& sb, uint32_t step) {
-#pragma unroll
-    for (int I = 0; I < IM; ++I)
-      sa[I] = *reinterpret_cast<const uint32_t*>(scale_a[I] + (uint64_t)step * a.lds);
-    sb = scale_b[(uint64_t)step * b.lds];
-  };
-
-  f32x4 acc[4 * IM][4] = {};
-  const uint32_t lo = r * kQ8Block + (2 * g ^ r / 2) * 16;
-  const uint32_t hi = r * kQ8Block + ((2 * g + 1) ^ r / 2) * 16;
-  auto frag = [&](const uint8_t* p) {
-    return join(*reinterpret_cast<const u32x4*>(p + lo), *reinterpret_cast<const u32x4*>(p + hi));
-  };
-  auto multiply = [&](const uint8_t* lds, const uint32_t (&sa)[IM], uint32_t sb) {
-    i32x8 fb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) fb[j] = frag(lds + (TM + wn + 16 * j) * kQ8Block);
-    i32x8 fa = frag(lds + wm * kQ8Block);
-#pragma unroll
-    for (int i = 0; i < 4 * IM; ++i) {
-      i32x8 next = fa;
-      if (i + 1 < 4 * IM) next = frag(lds + (wm + 16 * (i + 1)) * kQ8Block);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = mma<FA, FB>(fb[j], fa, acc[i][j], sb, sa[i / 4], i % 4);
-      fa = next;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // codes at or beyond K in the last block of the sum
-  auto clear_tail = [&](uint8_t* lds) {
-    const int left = (int)(K % kQ8Block);
-    for (uint32_t e = threadIdx.x; e < (TM + TN) * 8; e += 64 * kWaves) {
-      const int keep = left - 16 * (int)(e % 8 ^ e / 16 % 8);
-      if (keep >= 16) continue;
-      u32x4* at = reinterpret_cast<u32x4*>(lds + e * 16);
-      u32x4 v = *at;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        v[w] &= keep - 4 * w <= 0 ? 0u : keep - 4 * w >= 4 ? ~0u : (1u << 8 * (keep - 4 * w)) - 1;
-      *at = v;
-    }
-    drain_and_sync();
-  };
-
-  uint32_t sa[IM], sb, sa_next[IM], sb_next;
-  auto step = [&](uint8_t* here, uint8_t* there, uint32_t s) {
-    if (s + 1 < s1) {
-      load(there, s + 1);
-      load_scales(sa_next, sb_next, s + 1);
-    } else if ((s + 1) * kQ8Block > K) {
-      clear_tail(here);
-    }
-    multiply(here, sa, sb);
-    drain_and_sync();
-#pragma unroll
-    for (int I = 0; I < IM; ++I) sa[I] = sa_next[I];
-    sb = sb_next;
-  };
-  if (s0 < s1) {
-    load(lds, s0);
-    load_scales(sa, sb, s0);
-    drain_and_sync();
-    uint32_t half = 0;
-    for (uint32_t s = s0; s < s1; ++s) {
-      step(lds + half, lds + (kBytes - half), s);
-      half = kBytes - half;
-    }
+  for (int j = 0; j < kLoads; ++j) {
+    const bool is_a = j < kLoadsA;
+    const uint32_t p = (is_a ? wave * kLoadsA + j : wave * (kLoads - kLoadsA) + j - kLoadsA) * 8 + lane / 8;
+    const uint32_t row = is_a ? p / (32 * FM) * (32 * FM) + FM * (p % 32) + p / 32 % FM : p;
+    from[j] = row * (uint32_t)(is_a ? a.ld : b.ld) + (lane % 8 ^ spread(p)) * 16;
   }
 
-  c.data = static_cast<uint8_t*>(c.data) + t.part * part_bytes;
+  // The stream of blocks: the next one to load.  Rows beyond M and N lie beyond the views' ends.
+  struct {
+    uint32_t item, block, end;
+    uint64_t at_a, at_b, len_a, len_b;
+    const uint8_t *scale_a, *scale_b;
+  } in;
+  auto enter = [&](uint32_t item) {
+    in.item = item;
+    const TileAt t = tile_at(item, m_tiles, n_tiles, total);
+    const uint32_t m0 = t.row * TM, n0 = t.col * TN;
+    in.block = t.part * part_blocks;
+    in.end = min(in.block + part_blocks, blocks);
+    const uint64_t k = (uint64_t)in.block * kQ8Block;
+    in.at_a = (uint64_t)a.q + (uint64_t)m0 * a.ld + k;
+    in.at_b = (uint64_t)b.q + (uint64_t)n0 * b.ld + k;
+    in.len_a = (uint64_t)(M - m0) * a.ld - k;
+    in.len_b = (uint64_t)(N - n0) * b.ld - k;
+    in.scale_a = a.scale + in.block * a.lds + min(m0 + wm + FM * r, (uint32_t)a.lds - FM);
+    in.scale_b = b.scale + in.block * b.lds + min(n0 + wn, N - 1) / kQ8Block;
+  };
+  auto advance = [&] {
+    if (in.block + 1 < in.end) {
+      ++in.block;
+      in.at_a += kQ8Block, in.at_b += kQ8Block;
+      in.len_a -= kQ8Block, in.len_b -= kQ8Block;
+      in.scale_a += a.lds, in.scale_b += b.lds;
+    } else if (in.item + gridDim.x < total) {
+      enter(in.item + gridDim.x);
+    } else {
+      in.len_a = in.len_b = 0;  // nothing more: loads of zeros, and the last scales again
+    }
+  };
+  struct Views {
+    __amdgpu_buffer_rsrc_t a, b;
+  };
+  auto views = [&] { return Views{rsrc_of(in.at_a, in.len_a), rsrc_of(in.at_b, in.len_b)}; };
+  auto load = [&](uint8_t* to, const Views& v, int j) {
+    if (j < kLoadsA) load_to_lds(v.a, to + (wave * kLoadsA + j) * 1024, from[j]);
+    else load_to_lds(v.b, to + TM * kQ8Block + (wave * (kLoads - kLoadsA) + j - kLoadsA) * 1024, from[j]);
+  };
+  auto load_scales = [&](uint32_t& sa, uint32_t& sb) {
+    sa = FM == 4 ? *reinterpret_cast<const uint32_t*>(in.scale_a)
+                 : FM == 2 ? *reinterpret_cast<const uint16_t*>(in.scale_a) : *in.scale_a;
+    sb = *in.scale_b;
+  };
+
+  struct Frags {
+    i32x8 a[FM], b[FN];
+  };
+  uint32_t at[2][2];  // where in a fragment's rows this lane's pieces of a half lie
 #pragma unroll
-  for (int i = 0; i < 4 * IM; ++i) {
-    const uint32_t m = m0 + wm + 64 * (i / 4) + 4 * r + i % 4, n = n0 + wn + 16 * g;
-    if (m >= M || n >= N) continue;
-    float v[16];
+  for (int h = 0; h < 4; ++h)
+    at[h / 2][h % 2] = r * kQ8Block + ((h / 2 * 4 + 2 * g + h % 2) ^ spread(r)) * 16;
+  // read e of a half's 2 (FM + FN)
+  auto read = [&](Frags& f, const uint8_t* from_lds, int h, int e) {
+    const int i = e / 2;
+    const uint32_t row = i < FN ? TM + wn + 32 * i : wm + 32 * (i - FN);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(from_lds + row * kQ8Block + at[h][e % 2]);
+    i32x8& to = i < FN ? f.b[i] : f.a[i - FN];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = acc[i][e / 4][e % 4];
-    if (c.dtype == S2R_F32)
-      store16<S2R_F32>(static_cast<uint32_t*>(c.data) + (uint64_t)m * c.ld, n, N, v);
-    else if (c.dtype == S2R_BF16)
-      store16<S2R_BF16>(static_cast<uint16_t*>(c.data) + (uint64_t)m * c.ld, n, N, v);
-    else
-      store16<S2R_F16>(static_cast<uint16_t*>(c.data) + (uint64_t)m * c.ld, n, N, v);
+    for (int w = 0; w < 4; ++w) to[e % 2 * 4 + w] = (int)v[w];
+  };
+  auto clear_tail = [&](Frags& f, int left) {  // codes at or beyond K
+#pragma unroll
+    for (int i = 0; i < FM; ++i) clear_from(f.a[i], left - 32 * (int)g);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) clear_from(f.b[j], left - 32 * (int)g);
+  };
+  constexpr int kMma = FM * FN, kReads = 2 * (FM + FN);
+
+  uint8_t *here = lds, *there = lds + kBytes;
+  uint32_t sa = 0, sb = 0, sa_ahead = 0, sb_ahead = 0;  // of this block and of the next
+  Frags f0, f1;
+  if (blocks > 0) {
+    enter(blockIdx.x);
+    Views v = views();
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load(here, v, j);
+    load_scales(sa, sb);
+    advance();
+    v = views();
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load(there, v, j);
+    load_scales(sa_ahead, sb_ahead);
+    sync_but<kLoads>();
+#pragma unroll
+    for (int e = 0; e < kReads; ++e) read(f0, here, 0, e);
   }
+
+  for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const TileAt t = tile_at(item, m_tiles, n_tiles, total);
+    const uint32_t b0 = t.part * part_blocks, b1 = min(b0 + part_blocks, blocks);
+    f32x16 acc[FM][FN] = {};
+    auto multiply = [&](const Frags& f, int e) {
+      acc[e / FN][e % FN] = mma32<FA, FB>(f.b[e % FN], f.a[e / FN], acc[e / FN][e % FN], sb, sa, e / FN);
+    };
+    for (uint32_t block = b0; block < b1; ++block) {
+      advance();
+      if (TAIL) clear_tail(f0, (int)(K - block * kQ8Block));
+#pragma unroll
+      for (int e = 0; e < kMma; ++e) {
+        multiply(f0, e);
+#pragma unroll
+        for (int q = e * kReads / kMma; q < (e + 1) * kReads / kMma; ++q) read(f1, here, 1, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      drain_and_sync();  // the next block is there, and this one's LDS is free
+      const uint32_t sa_next = sa_ahead, sb_next = sb_ahead;
+      load_scales(sa_ahead, sb_ahead);
+      const Views v = views();
+      if (TAIL) clear_tail(f1, (int)(K - block * kQ8Block) - 64);
+#pragma unroll
+      for (int e = 0; e < kMma; ++e) {
+        multiply(f1, e);
+#pragma unroll
+        for (int q = e * kReads / kMma; q < (e + 1) * kReads / kMma; ++q) read(f0, there, 0, q);
+#pragma unroll
+        for (int q = e * kLoads / kMma; q < (e + 1) * kLoads / kMma; ++q) load(here, v, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      uint8_t* const x = here;
+      here = there;
+      there = x;
+      sa = sa_next;
+      sb = sb_next;
+    }
+    // 32 x 64 results at a time turn in LDS, so that whole lines leave; piece s of row p is at
+    // s ^ (p % 8, p / 16)
+    const uint32_t m0 = t.row * TM + wm, n0 = t.col * TN + wn;  // of this wave
+    if (m0 >= M || n0 >= N) continue;
+    uint8_t* const mine = lds + 2 * kBytes + wave * kTurn;
+    const uint32_t mix = r % 8 | r / 16 * 8;
+    s2r_mat out = c;
+    out.data = static_cast<uint8_t*>(c.data) + t.part * part_bytes;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; j += 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const f32x16& x = acc[i][j + e / 4];
+          const int q = e % 4 * 4;
+          *reinterpret_cast<f32x4*>(mine + r * 256 + ((2 * e + g) ^ mix) * 16) =
+              f32x4{x[q], x[q + 1], x[q + 2], x[q + 3]};
+        }
+        __builtin_amdgcn_wave_barrier();
+        store_turned(out, mine, m0 + i, FM, M, n0 + 32 * j, N);
+        __builtin_amdgcn_wave_barrier();
+      }
+  }
+  drain_and_sync();
+}
+
+// ---- few rows: fragments of 16 rows --------------------------------------------------------
+template <int FA, int FB>
+__device__ inline f32x4 mma(const i32x8& b, const i32x8& a, const f32x4& c, uint32_t sb, uint32_t sa) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 0, (int)sa);
 }
 
 // ---- few rows -----------------------------------------------------------------------------
@@ -230,7 +343,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
       if (s + e * WAVES >= steps) continue;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
-        acc[i] = mma<FA, FB>(fb[e], fa[e][i], acc[i], sb[e], sa[e][i], 0);
+        acc[i] = mma<FA, FB>(fb[e], fa[e][i], acc[i], sb[e], sa[e][i]);
     }
   }
 #pragma unroll
@@ -265,9 +378,22 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
     return;
   }
   trace_mark(s, "k_q8_gemm");
-  const uint32_t mt = (m + 255) / 256, nt = (n + 255) / 256, steps = (k + kQ8Block - 1) / kQ8Block;
-  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 4, 2>), dim3(mt * nt), dim3(512), 0, s, a, b, c, 0, m, n,
-                     k, mt, nt, steps);
+  const uint32_t blocks = (k + kQ8Block - 1) / kQ8Block;
+#ifdef V2
+  const uint32_t mt = (m + 255) / 256, nt = (n + 127) / 128;
+  constexpr int FN = 2;
+#else
+  const uint32_t mt = (m + 255) / 256, nt = (n + 255) / 256;
+  constexpr int FN = 4;
+#endif
+  const uint32_t total = mt * nt;
+  const dim3 grid(min(total, kTileCus));
+  if (k % kQ8Block == 0)
+    hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, 4, FN, false>), grid, dim3(256), 0, s, a, b, c, 0,
+                     m, n, k, mt, nt, total, blocks);
+  else
+    hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, 4, FN, true>), grid, dim3(256), 0, s, a, b, c, 0,
+                     m, n, k, mt, nt, total, blocks);
 }
 
 }  // namespace

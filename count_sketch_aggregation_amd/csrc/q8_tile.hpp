@@ -14,7 +14,8 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 // A bounds-checked view of global memory: reads at or beyond `bytes` give zeros.
 __device__ inline __amdgpu_buffer_rsrc_t rsrc_of(uint64_t base, uint64_t bytes) {
-  const uint32_t n = bytes > 0xffffffffull ? 0xffffffffu : (uint32_t)bytes;
+  // offsets of a tile stay below 2^31 + 2^30: what ends beyond may as well end there
+  const uint32_t n = bytes > 0xc0000000ull ? 0xc0000000u : (uint32_t)bytes;
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, (int)n, 0x00020000);
 }
 
@@ -32,10 +33,20 @@ __device__ inline void drain_and_sync() {
   asm volatile("" ::: "memory");
 }
 
-// Workgroup b of `total` to a tile and a part of the sum.  Consecutive workgroups go to
-// the eight accelerator dies in turn, so the work list is cut into eight stretches, one for
-// each die and its L2; within a stretch kTileGroup rows of tiles are walked column by column,
-// so that the workgroups that run together on a die share rows and columns of both operands.
+// The same with the wave's newest LEFT loads still on their way.
+template <int LEFT>
+__device__ inline void sync_but() {
+  static_assert(LEFT >= 0 && LEFT < 64, "six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Item b of `total` to a tile and a part of the sum.  Consecutive workgroups go to the eight
+// accelerator dies in turn, so the items are cut into eight stretches, one for each die and
+// its L2; within a stretch kTileGroup rows of tiles are walked column by column, so that the
+// workgroups that run together on a die share rows and columns of both operands.
 struct TileAt {
   uint32_t row, col, part;
 };
@@ -49,6 +60,10 @@ __device__ inline TileAt tile_at(uint32_t b, uint32_t rows, uint32_t cols, uint3
   const uint32_t height = min(rows - first, kTileGroup), in = lin - g * span;
   t.row = first + in % height;
   t.col = in / height;
+  // divisions run in vector registers: back to scalar ones
+  t.row = __builtin_amdgcn_readfirstlane(t.row);
+  t.col = __builtin_amdgcn_readfirstlane(t.col);
+  t.part = __builtin_amdgcn_readfirstlane(t.part);
   return t;
 }
 
