@@ -136,50 +136,61 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     from[j] = row * (uint32_t)(is_a ? a.ld : b.ld) + (lane % 8 ^ spread(p)) * 16;
   }
 
-  // The stream of blocks: the next one to load.  Rows beyond M and N lie beyond the views' ends.
-  struct {
-    uint32_t item, block, end;
-    uint64_t at_a, at_b, len_a, len_b;
-    const uint8_t *scale_a, *scale_b;
-  } in;
-  auto enter = [&](uint32_t item) {
-    in.item = item;
-    const TileAt t = tile_at(item, m_tiles, n_tiles, total);
-    const uint32_t m0 = t.row * TM, n0 = t.col * TN;
-    in.block = t.part * part_blocks;
-    in.end = min(in.block + part_blocks, blocks);
-    const uint64_t k = (uint64_t)in.block * kQ8Block;
-    in.at_a = (uint64_t)a.q + (uint64_t)m0 * a.ld + k;
-    in.at_b = (uint64_t)b.q + (uint64_t)n0 * b.ld + k;
-    in.len_a = (uint64_t)(M - m0) * a.ld - k;
-    in.len_b = (uint64_t)(N - n0) * b.ld - k;
-    in.scale_a = a.scale + in.block * a.lds + min(m0 + wm + FM * r, (uint32_t)a.lds - FM);
-    in.scale_b = b.scale + in.block * b.lds + min(n0 + wn, N - 1) / kQ8Block;
+  // The stream of blocks: the newest that is loaded, and the first one of the item after its
+  // own.  Rows beyond M and N lie beyond the views' ends.
+  struct At {
+    uint32_t item, left;  // blocks of the item after this one
+    uint64_t a, b, len_a, len_b, scale_a;
+    uint64_t scale_b;
+    uint32_t lane_scale;
   };
-  auto advance = [&] {
-    if (in.block + 1 < in.end) {
-      ++in.block;
-      in.at_a += kQ8Block, in.at_b += kQ8Block;
-      in.len_a -= kQ8Block, in.len_b -= kQ8Block;
-      in.scale_a += a.lds, in.scale_b += b.lds;
-    } else if (in.item + gridDim.x < total) {
-      enter(in.item + gridDim.x);
-    } else {
-      in.len_a = in.len_b = 0;  // nothing more: loads of zeros, and the last scales again
-    }
+  auto start_of = [&](uint32_t item) {
+    At x = {};
+    x.item = item;
+    x.left = ~0u;  // nothing more: loads of zeros, and some scales or other
+    x.scale_a = (uint64_t)a.scale;
+    x.scale_b = (uint64_t)b.scale;
+    if (item >= total) return x;
+    const TileAt t = tile_at(item, m_tiles, n_tiles, total);
+    const uint32_t m0 = t.row * TM, n0 = t.col * TN, block = t.part * part_blocks;
+    const uint64_t k = (uint64_t)block * kQ8Block;
+    x.left = __builtin_amdgcn_readfirstlane(min(block + part_blocks, blocks) - block - 1);
+    x.a = (uint64_t)a.q + (uint64_t)m0 * a.ld + k;
+    x.b = (uint64_t)b.q + (uint64_t)n0 * b.ld + k;
+    x.len_a = (uint64_t)(M - m0) * a.ld - k;
+    x.len_b = (uint64_t)(N - n0) * b.ld - k;
+    x.scale_a += block * a.lds;
+    x.scale_b += block * b.lds + min(n0 + wn, N - 1) / kQ8Block;
+    x.lane_scale = min(m0 + wm + FM * r, (uint32_t)a.lds - FM);
+    return x;
+  };
+  At in, after;
+  auto advance = [&] {  // without a branch: it runs between matrix instructions
+    in.left = __builtin_amdgcn_readfirstlane(in.left);
+    const bool go = in.left == 0, on = in.left + 1 > 1;
+    in.item = go ? after.item : in.item;
+    in.a = go ? after.a : in.a + kQ8Block;
+    in.b = go ? after.b : in.b + kQ8Block;
+    in.len_a = go ? after.len_a : on ? in.len_a - kQ8Block : 0;
+    in.len_b = go ? after.len_b : on ? in.len_b - kQ8Block : 0;
+    in.scale_a = go ? after.scale_a : on ? in.scale_a + a.lds : in.scale_a;
+    in.scale_b = go ? after.scale_b : on ? in.scale_b + b.lds : in.scale_b;
+    in.lane_scale = go ? after.lane_scale : in.lane_scale;
+    in.left = go ? after.left : on ? in.left - 1 : ~0u;
   };
   struct Views {
     __amdgpu_buffer_rsrc_t a, b;
   };
-  auto views = [&] { return Views{rsrc_of(in.at_a, in.len_a), rsrc_of(in.at_b, in.len_b)}; };
+  auto views = [&] { return Views{rsrc_of(in.a, in.len_a), rsrc_of(in.b, in.len_b)}; };
   auto load = [&](uint8_t* to, const Views& v, int j) {
     if (j < kLoadsA) load_to_lds(v.a, to + (wave * kLoadsA + j) * 1024, from[j]);
     else load_to_lds(v.b, to + TM * kQ8Block + (wave * (kLoads - kLoadsA) + j - kLoadsA) * 1024, from[j]);
   };
   auto load_scales = [&](uint32_t& sa, uint32_t& sb) {
-    sa = FM == 4 ? *reinterpret_cast<const uint32_t*>(in.scale_a)
-                 : FM == 2 ? *reinterpret_cast<const uint16_t*>(in.scale_a) : *in.scale_a;
-    sb = *in.scale_b;
+    const uint8_t* at = reinterpret_cast<const uint8_t*>(in.scale_a) + in.lane_scale;
+    sa = FM == 4 ? *reinterpret_cast<const uint32_t*>(at)
+                 : FM == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
+    sb = *reinterpret_cast<const uint8_t*>(in.scale_b);
   };
 
   struct Frags {
@@ -205,12 +216,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     for (int j = 0; j < FN; ++j) clear_from(f.b[j], left - 32 * (int)g);
   };
   constexpr int kMma = FM * FN, kReads = 2 * (FM + FN);
+  constexpr int kRead = kMma * 5 / 16, kEarly = kLoads * 5 / 8;  // when reads end and loads begin
 
   uint8_t *here = lds, *there = lds + kBytes;
   uint32_t sa = 0, sb = 0, sa_ahead = 0, sb_ahead = 0;  // of this block and of the next
   Frags f0, f1;
   if (blocks > 0) {
-    enter(blockIdx.x);
+    in = start_of(blockIdx.x);
+    after = start_of(blockIdx.x + gridDim.x);
     Views v = views();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) load(here, v, j);
@@ -228,32 +241,45 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
     const TileAt t = tile_at(item, m_tiles, n_tiles, total);
     const uint32_t b0 = t.part * part_blocks, b1 = min(b0 + part_blocks, blocks);
+    after = start_of(in.item + gridDim.x);
     f32x16 acc[FM][FN] = {};
     auto multiply = [&](const Frags& f, int e) {
       acc[e / FN][e % FN] = mma32<FA, FB>(f.b[e % FN], f.a[e / FN], acc[e / FN][e % FN], sb, sa, e / FN);
     };
     for (uint32_t block = b0; block < b1; ++block) {
-      advance();
       if (TAIL) clear_tail(f0, (int)(K - block * kQ8Block));
 #pragma unroll
-      for (int e = 0; e < kMma; ++e) {
+      for (int e = 0; e < kRead; ++e) {
         multiply(f0, e);
 #pragma unroll
-        for (int q = e * kReads / kMma; q < (e + 1) * kReads / kMma; ++q) read(f1, here, 1, q);
+        for (int q = e * kReads / kRead; q < (e + 1) * kReads / kRead; ++q) read(f1, here, 1, q);
+        if (e == 0) advance();
         __builtin_amdgcn_sched_barrier(0);
       }
-      drain_and_sync();  // the next block is there, and this one's LDS is free
-      const uint32_t sa_next = sa_ahead, sb_next = sb_ahead;
-      load_scales(sa_ahead, sb_ahead);
+      multiply(f0, kRead);
+      sync_reads();  // this block's LDS is free
       const Views v = views();
+#pragma unroll
+      for (int e = kRead + 1; e < kMma; ++e) {
+        multiply(f0, e);
+#pragma unroll
+        for (int q = (e - kRead - 1) * kEarly / (kMma - kRead - 1); q < (e - kRead) * kEarly / (kMma - kRead - 1); ++q)
+          load(here, v, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sync_but<kEarly>();  // the next block is there
+      // moved here, where their loads are known to be done, and not by the compiler further up
+      uint32_t sa_next, sb_next;
+      asm volatile("v_mov_b32 %0, %1" : "=v"(sa_next) : "v"(sa_ahead));
+      asm volatile("v_mov_b32 %0, %1" : "=v"(sb_next) : "v"(sb_ahead));
+      load_scales(sa_ahead, sb_ahead);
       if (TAIL) clear_tail(f1, (int)(K - block * kQ8Block) - 64);
 #pragma unroll
       for (int e = 0; e < kMma; ++e) {
         multiply(f1, e);
 #pragma unroll
         for (int q = e * kReads / kMma; q < (e + 1) * kReads / kMma; ++q) read(f0, there, 0, q);
-#pragma unroll
-        for (int q = e * kLoads / kMma; q < (e + 1) * kLoads / kMma; ++q) load(here, v, q);
+        if (kEarly + e < kLoads) load(here, v, kEarly + e);
         __builtin_amdgcn_sched_barrier(0);
       }
       uint8_t* const x = here;

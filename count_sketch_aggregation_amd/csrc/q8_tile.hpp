@@ -43,6 +43,14 @@ __device__ inline void sync_but() {
   asm volatile("" ::: "memory");
 }
 
+// Every LDS access of all waves is done; loads may be on their way.
+__device__ inline void sync_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Item b of `total` to a tile and a part of the sum.  Consecutive workgroups go to the eight
 // accelerator dies in turn, so the items are cut into eight stretches, one for each die and
 // its L2; within a stretch kTileGroup rows of tiles are walked column by column, so that the
