@@ -75,4 +75,42 @@ __device__ inline TileAt tile_at(uint32_t b, uint32_t rows, uint32_t cols, uint3
   return t;
 }
 
+// 32 x 64 fp32 results from LDS, laid out as the products leave them (16-byte piece s of row p
+// at s ^ (p % 8, p / 16)), to rows n0 .., columns k0 .. of dw, or added to what is there.  Four
+// columns per lane, 16 lanes a row; dw is only known to be 4-byte aligned.
+__device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, uint32_t n0, uint32_t N,
+                                  uint32_t k0, uint32_t K, bool accumulate) {
+  if (n0 >= N || k0 >= K) return;
+  typedef f32x4 __attribute__((aligned(4))) f32x4_a4;
+  const uint32_t lane = threadIdx.x % 64, s = lane % 16, k = k0 + 4 * s;
+  f32x4 v[8];
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e) {
+    const uint32_t row = lane / 16 + 4 * e, mix = row % 8 | row / 16 * 8;
+    v[e] = *reinterpret_cast<const f32x4*>(lds + row * 256 + (s ^ mix) * 16);
+  }
+  float* const at = dw + (uint64_t)(n0 + lane / 16) * ld + k;
+  if (n0 + 32 <= N && k0 + 64 <= K) {
+    if (accumulate) {
+      f32x4 old[8];
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) old[e] = *reinterpret_cast<const f32x4_a4*>(at + 4 * e * ld);
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) v[e] += old[e];
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e) *reinterpret_cast<f32x4_a4*>(at + 4 * e * ld) = v[e];
+    return;
+  }
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e) {
+    if (n0 + lane / 16 + 4 * e >= N) continue;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c) {
+      float* const p = at + 4 * e * ld + c;
+      if (k + c < K) *p = accumulate ? *p + v[e][c] : v[e][c];
+    }
+  }
+}
+
 }  // namespace s2r

@@ -3,88 +3,294 @@
 // The checkpoint's scale changes along m, the summed index, so the scaled matrix instruction
 // cannot apply it: both operands become bf16, which holds every stored value exactly, and
 // the products are summed in fp32 by the bf16 matrix instruction.
-#include "q8_device.hpp"
 #include "q8_launch.hpp"
+#include "q8_tile.hpp"
 
 namespace s2r {
 
-constexpr int kWgradThreads = 256;  // 4 waves, each 32 x 32 of a 64 x 64 tile
+constexpr int kWgradRows = 64;  // rows m of a block of the sum
+constexpr int kBf16 = 2;        // kind of an operand that is bf16 already (else its q8 format)
 
-// element (m, c) of an operand as bf16 bits; zero at or beyond M
-template <int KIND>  // 0, 1: row-block codes of that format; 2: bf16
-__device__ inline uint16_t wgrad_elem(const s2r_mat& d, const s2r_q8_mat& q, uint32_t m, uint32_t c,
-                                      uint32_t M) {
-  if (m >= M) return 0;
-  if (KIND == 2) return static_cast<const uint16_t*>(d.data)[(uint64_t)m * d.ld + c];
-  const int code = q.q[(uint64_t)m * q.ld + c];
-  const float s = scale_value(q.scale[(uint64_t)(c / kQ8Block) * q.lds + m]);
-  const float v = (KIND == S2R_E4M3 ? __builtin_amdgcn_cvt_f32_fp8(code, 0)
-                                    : __builtin_amdgcn_cvt_f32_bf8(code, 0)) * s;
-  return (uint16_t)(__float_as_uint(v) >> 16);  // exact
+// 16 codes to bf16: exact, as a scale is a power of two and a stored value a normal bf16.
+template <int FMT>
+__device__ inline void to_bf16(u32x4 q, float scale, u32x4& lo, u32x4& hi) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t a, b;
+    if (FMT == S2R_E4M3) {
+      a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[w], scale, false));
+      b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[w], scale, true));
+    } else {
+      a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[w], scale, false));
+      b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[w], scale, true));
+    }
+    (w < 2 ? lo : hi)[w % 2 * 2] = a;
+    (w < 2 ? lo : hi)[w % 2 * 2 + 1] = b;
+  }
 }
 
-template <int KY, int FX>
-__global__ __launch_bounds__(kWgradThreads) void k_q8_wgrad(s2r_mat dy16, s2r_q8_mat dy8,
-                                                            s2r_q8_mat x, float* dw, uint64_t lddw,
-                                                            uint32_t M, uint32_t N, uint32_t K,
-                                                            bool accumulate, uint32_t k_tiles) {
-  const uint32_t wave = threadIdx.x / 64, r = threadIdx.x % 16, g = threadIdx.x % 64 / 16;
-  const uint32_t n0 = blockIdx.x / k_tiles * 64 + wave / 2 * 32;
-  const uint32_t k0 = blockIdx.x % k_tiles * 64 + wave % 2 * 32;
-  f32x4 acc[2][2] = {};
-  for (uint32_t m = 0; m < M; m += 32) {
-    bf16x8 fy[2], fx[2];
+// An operand on its way to LDS, a block of 64 rows x COLS columns at a time, bf16 there: 64-byte
+// piece s of row p lies at s ^ (p % 4).  What is bf16 already goes there directly; codes come
+// to registers first and are decoded from there.  Rows at or beyond the end give zeros.
+template <int KIND, int COLS, int WAVES>
+struct Feed {
+  static constexpr bool kDirect = KIND == kBf16;
+  static constexpr int kRowBytes = 2 * COLS, kBytes = kWgradRows * kRowBytes;
+  static constexpr int kSource = kDirect ? kRowBytes : COLS;  // bytes of a row where it comes from
+  static constexpr int kLoads = kWgradRows * kSource / 1024 / WAVES, kRows = 1024 / kSource;
+  static_assert(kLoads > 0 && kLoads * kRows % 4 == 0, "");
+
+  uint64_t base, left, step;  // the next block: address, bytes to the operand's end, its own bytes
+  uint32_t at[kLoads];        // of this lane in each load
+  uint32_t wave, row, last;
+  const uint8_t* scale;
+  uint32_t to;                // LDS place of this lane's first codes
+  u32x4 code[kLoads];
+  uint32_t sb[kLoads];
+
+  __device__ void start(const s2r_mat& m, const s2r_q8_mat& q, uint32_t c0, uint32_t cols,
+                        uint32_t first, uint32_t end, uint32_t w) {
+    const uint32_t lane = threadIdx.x % 64, s = lane % (kSource / 16), r = lane / (kSource / 16);
+    const uint32_t ld = kDirect ? (uint32_t)m.ld * 2 : (uint32_t)q.ld;
+    const uint64_t skip = kDirect ? 2 * (uint64_t)c0 : c0;
+    wave = w;
+    base = (kDirect ? (uint64_t)m.data : (uint64_t)q.q) + (uint64_t)first * ld + skip;
+    const uint64_t all = (uint64_t)(end - first) * ld;
+    left = all > skip ? all - skip : 0;
+    step = (uint64_t)kWgradRows * ld;
+    const uint32_t p0 = wave * (kLoads * kRows) + r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t n = min(n0 + 16 * i + r, N - 1), k = min(k0 + 16 * i + r, K - 1);
+    for (int j = 0; j < kLoads; ++j) {
+      const uint32_t p = p0 + j * kRows;
+      at[j] = p * ld + (kDirect ? (s / 4 ^ p % 4) * 64 + s % 4 * 16 : s * 16);
+    }
+    if (!kDirect) {
+      row = first + p0;
+      last = end - 1;
+      scale = q.scale + (uint64_t)(min(c0 + 16 * s, cols - 1) / kQ8Block) * q.lds;
+      to = p0 * kRowBytes + (s / 2 ^ p0 % 4) * 64 + s % 2 * 32;
+    }
+  }
+  __device__ void advance() {
+    base += step;
+    left = left > step ? left - step : 0;
+  }
+  __device__ __amdgpu_buffer_rsrc_t view() const { return rsrc_of(base, left); }
+  // The compiler would have every transposing load of LDS wait for every load that is on its
+  // way there: it is not told of these, and the loop waits for them itself.  Nothing comes back
+  // to a register; the pause covers scalar registers that a vector instruction has just written.
+  __device__ void load(uint8_t* lds, u32x4 v, int j) const {
+    const uint32_t to = (uint32_t)(uintptr_t)(lds_void*)(lds + (wave * kLoads + j) * 1024);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at[j]), "s"(v) : "memory");
+  }
+  __device__ u32x4 words() const {
+    const uint32_t n = left > 0xc0000000ull ? 0xc0000000u : (uint32_t)left;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)base),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32) & 0xffffu),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
+  }
+  // codes of the next block, with their scales (of a row beyond the end: any, its codes are 0)
+  __device__ void fetch() {
+    const auto v = view();
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, at[j], 0, 0));
+      sb[j] = scale[min(row + j * kRows, last)];
+    }
+    row += kWgradRows;
+  }
+  // Piece j decoded.  Half of the lanes write their upper half first: together the lanes of a
+  // write then meet every bank.
+  __device__ void decode(uint8_t* lds, int j) const {
+    const bool swap = threadIdx.x / 8 % 2;
+    const u32x4 c = code[j];
+    u32x4 lo, hi;
+    to_bf16 < KIND == S2R_E5M2 ? S2R_E5M2 : S2R_E4M3 > (u32x4{swap ? c[2] : c[0], swap ? c[3] : c[1],
+            swap ? c[0] : c[2], swap ? c[1] : c[3]}, scale_value(sb[j]), lo, hi);
+    uint8_t* p = lds + to + j * (kRows * kRowBytes);
+    *reinterpret_cast<u32x4*>(p + (swap ? 16 : 0)) = lo;
+    *reinterpret_cast<u32x4*>(p + (swap ? 0 : 16)) = hi;
+  }
+};
+
+// WM x WN waves, each 32 FM columns n by 32 FN columns k of dw; a block is 64 rows m, summed in
+// four steps of 16.  The matrix instruction wants eight rows m of one column in a lane, and
+// memory has columns side by side: LDS is read with the transposing load, four rows of 16
+// columns to a lane each.  LDS holds two blocks of both operands; the fragments of a step are
+// read while the step before is multiplied, so a block's LDS is free before its last step:
+// there the block after the next begins to arrive, and its codes, which came to registers
+// meanwhile, are decoded.
+template <int KY, int FX, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_wgrad(
+    s2r_mat dy16, s2r_q8_mat dy8, s2r_q8_mat xq, float* dw, uint64_t lddw, uint64_t part_floats,
+    uint32_t M, uint32_t N, uint32_t K, bool accumulate, uint32_t n_tiles, uint32_t k_tiles,
+    uint32_t part_rows) {
+  constexpr int kWaves = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
+  using Y = Feed<KY, TM, kWaves>;
+  using X = Feed<FX, TN, kWaves>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (Y::kBytes + X::kBytes)];
+
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
+  const TileAt t = tile_at(blockIdx.x, n_tiles, k_tiles, gridDim.x);
+  const uint32_t n0 = t.row * TM, k0 = t.col * TN;
+  const uint32_t wm = wave / WN * (32 * FM), wn = wave % WN * (32 * FN);
+  const uint32_t m0 = t.part * part_rows, m1 = min(m0 + part_rows, M);
+
+  struct Frags {
+    bf16x8 y[FM], x[FN];
+  };
+  // read e of a step's 2 (FM + FN), two for a fragment
+  const uint32_t q = lane % 16;
+  uint32_t at_y[FM], at_x[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+    at_y[i] = (8 * g + q / 4) * Y::kRowBytes + ((wm / 32 + i) ^ q / 4) * 64 + lane / 16 % 2 * 32 + q % 4 * 8;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    at_x[j] = (8 * g + q / 4) * X::kRowBytes + ((wn / 32 + j) ^ q / 4) * 64 + lane / 16 % 2 * 32 + q % 4 * 8;
+  auto read = [&](Frags& f, const uint8_t* ly, const uint8_t* lx, int step, int e) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int i = e / 2;
+    const uint8_t* p = i < FN ? lx + at_x[i] + (16 * step + e % 2 * 4) * X::kRowBytes
+                              : ly + at_y[i - FN] + (16 * step + e % 2 * 4) * Y::kRowBytes;
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    bf16x8& to = i < FN ? f.x[i] : f.y[i - FN];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) to[e % 2 * 4 + w] = __builtin_bit_cast(__bf16, (short)v[w]);
+  };
+  constexpr int kMma = FM * FN, kReads = 2 * (FM + FN);
+  f32x16 acc[FM][FN] = {};
+
+  if (m0 < m1) {
+    Y y;
+    X x;
+    y.start(dy16, dy8, n0, N, m0, m1, wave);
+    x.start(dy16, xq, k0, K, m0, m1, wave);
+    uint8_t *here = lds, *there = lds + (Y::kBytes + X::kBytes);
+    auto load_y = [&](uint8_t* to, int e, int of) {  // share e of a block
+      if (!Y::kDirect) return;
+      const u32x4 v = y.words();
+#pragma unroll
+      for (int j = e * Y::kLoads / of; j < (e + 1) * Y::kLoads / of; ++j) y.load(to, v, j);
+      if (e == of - 1) y.advance();
+    };
+    auto fetch = [&] {
+      x.fetch();
+      x.advance();
+      if (!Y::kDirect) {
+        y.fetch();
+        y.advance();
+      }
+    };
+    constexpr int kPieces = X::kLoads + (Y::kDirect ? 0 : Y::kLoads);
+    auto decode = [&](uint8_t* to, int e, int of) {
+#pragma unroll
+      for (int j = e * kPieces / of; j < (e + 1) * kPieces / of; ++j) {
+        if (j < X::kLoads) x.decode(to + Y::kBytes, j);
+        else if (!Y::kDirect) y.decode(to, j - X::kLoads);
+      }
+    };
+    fetch();
+    load_y(here, 0, 1);
+    decode(here, 0, 1);
+    fetch();
+    load_y(there, 0, 1);
+    decode(there, 0, 1);
+    fetch();
+    drain_and_sync();
+    Frags f0, f1;
+#pragma unroll
+    for (int e = 0; e < kReads; ++e) read(f0, here, here + Y::kBytes, 0, e);
+
+    auto multiply = [&](const Frags& f, int e) {
+      acc[e / FN][e % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[e % FN], f.y[e / FN], acc[e / FN][e % FN], 0, 0, 0);
+    };
+    auto step = [&](const Frags& f, Frags& next, int s) {
+#pragma unroll
+      for (int e = 0; e < kMma; ++e) {
+        multiply(f, e);
+#pragma unroll
+        for (int i = e * kReads / kMma; i < (e + 1) * kReads / kMma; ++i)
+          read(next, here, here + Y::kBytes, s + 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (uint32_t m = m0; m < m1; m += kWgradRows) {
+      step(f0, f1, 0);
+      step(f1, f0, 1);
+      step(f0, f1, 2);
+      drain_and_sync();  // the next block is there, codes are in registers, this LDS is free
+#pragma unroll
+      for (int e = 0; e < kMma; ++e) {
+        multiply(f1, e);
+#pragma unroll
+        for (int i = e * kReads / kMma; i < (e + 1) * kReads / kMma; ++i)
+          read(f0, there, there + Y::kBytes, 0, i);
+        load_y(here, e, kMma);
+        decode(here, e, kMma);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      fetch();
+      uint8_t* const t = here;
+      here = there;
+      there = t;
+    }
+  }
+  drain_and_sync();
+
+  // Lane (r, g) of a fragment holds column n = r, columns k = 8 (i / 4) + 4 g + i % 4; 32 x 64 at a
+  // time turn in LDS, so that whole lines leave.
+  constexpr int kTurn = 32 * 64 * 4;
+  static_assert(kWaves * kTurn <= (int)sizeof(lds), "");
+  uint8_t* const mine = lds + wave * kTurn;
+  const uint32_t mix = r % 8 | r / 16 * 8;
+  float* const out = dw + t.part * part_floats;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t mm = m + 8 * g + e;
-        fy[i][e] = __builtin_bit_cast(__bf16, wgrad_elem<KY>(dy16, dy8, mm, n, M));
-        fx[i][e] = __builtin_bit_cast(__bf16, wgrad_elem<FX>(dy16, x, mm, k, M));
+        const f32x16& v = acc[i][j + e / 4];
+        const int w = e % 4 * 4;
+        *reinterpret_cast<f32x4*>(mine + r * 256 + ((2 * e + g) ^ mix) * 16) = f32x4{v[w], v[w + 1], v[w + 2], v[w + 3]};
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[j], fy[i], acc[i][j], 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t n = n0 + 16 * i + r;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t k = k0 + 16 * j + 4 * g + t;
-        if (n >= N || k >= K) continue;
-        float* at = dw + (uint64_t)n * lddw + k;
-        *at = accumulate ? *at + acc[i][j][t] : acc[i][j][t];
-      }
+      __builtin_amdgcn_wave_barrier();
+      add_turned(out, lddw, mine, n0 + wm + 32 * i, N, k0 + wn + 32 * j, K, accumulate);
+      __builtin_amdgcn_wave_barrier();
     }
 }
 
 size_t q8_wgrad_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
 
+namespace {
+
+template <int KY, int FX>
+void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8_mat& q,
+              const s2r_q8_mat& x, float* dw, uint64_t lddw, bool accumulate, hipStream_t s) {
+  const uint32_t nt = (uint32_t)((N + 255) / 256), kt = (uint32_t)((K + 255) / 256);
+  hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 4, 4>), dim3(nt * kt), dim3(256), 0, s, d, q, x, dw,
+                     lddw, 0, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, (uint32_t)M);
+}
+
+}  // namespace
+
 hipError_t launch_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy16,
                            const s2r_q8_mat* dy8, const s2r_q8_mat& x, float* dw, uint64_t lddw,
                            bool accumulate, void*, hipStream_t s) {
-  const uint64_t kt = (K + 63) / 64, nt = (N + 63) / 64;
   const s2r_mat d = dy16 ? *dy16 : s2r_mat{};
   const s2r_q8_mat q = dy8 ? *dy8 : s2r_q8_mat{};
   trace_mark(s, "k_q8_wgrad");
-#define S2R_WGRAD(KY, FX)                                                               \
-  hipLaunchKernelGGL((k_q8_wgrad<KY, FX>), dim3((uint32_t)(nt * kt)), dim3(kWgradThreads), 0, \
-                     s, d, q, x, dw, lddw, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate,  \
-                     (uint32_t)kt)
-  const int ky = dy16 ? 2 : (int)dy8->format;
+#define S2R_WGRAD(KY, FX) go_wgrad<KY, FX>(M, N, K, d, q, x, dw, lddw, accumulate, s)
+  const int ky = dy16 ? kBf16 : (int)dy8->format;
   if (x.format == S2R_E4M3) {
-    if (ky == 2) S2R_WGRAD(2, S2R_E4M3);
+    if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E4M3);
     else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E4M3);
     else S2R_WGRAD(S2R_E5M2, S2R_E4M3);
   } else {
-    if (ky == 2) S2R_WGRAD(2, S2R_E5M2);
+    if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E5M2);
     else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E5M2);
     else S2R_WGRAD(S2R_E5M2, S2R_E5M2);
   }
