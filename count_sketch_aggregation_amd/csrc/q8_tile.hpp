@@ -113,4 +113,14 @@ __device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, ui
   }
 }
 
+// A sum cut into parts of whole blocks, each with its own partial results.
+struct Cut {
+  uint32_t parts, blocks;  // blocks of a part
+};
+inline Cut cut_evenly(uint32_t blocks, uint32_t parts) {
+  if (blocks == 0) return {1, 0};
+  const uint32_t each = (blocks + parts - 1) / parts;
+  return {(blocks + each - 1) / each, each};
+}
+
 }  // namespace s2r

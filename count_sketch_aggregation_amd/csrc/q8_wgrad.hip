@@ -3,6 +3,8 @@
 // The checkpoint's scale changes along m, the summed index, so the scaled matrix instruction
 // cannot apply it: both operands become bf16, which holds every stored value exactly, and
 // the products are summed in fp32 by the bf16 matrix instruction.
+#include <algorithm>
+
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
@@ -122,7 +124,7 @@ struct Feed {
 // there the block after the next begins to arrive, and its codes, which came to registers
 // meanwhile, are decoded.
 template <int KY, int FX, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_wgrad(
+__global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
     s2r_mat dy16, s2r_q8_mat dy8, s2r_q8_mat xq, float* dw, uint64_t lddw, uint64_t part_floats,
     uint32_t M, uint32_t N, uint32_t K, bool accumulate, uint32_t n_tiles, uint32_t k_tiles,
     uint32_t part_rows) {
@@ -263,27 +265,99 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_wgrad(
     }
 }
 
-size_t q8_wgrad_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
+// The partial sums of a row, added in their order.
+constexpr int kSumThreads = 256;
+__global__ __launch_bounds__(kSumThreads) void k_q8_wgrad_sum(const float* __restrict__ part,
+                                                              uint64_t part_floats, uint32_t parts,
+                                                              float* __restrict__ dw, uint64_t lddw,
+                                                              uint32_t N, uint32_t K, bool accumulate) {
+  typedef f32x4 __attribute__((aligned(4))) f32x4_a4;
+  const uint32_t quads = (K + 3) / 4;
+  const uint64_t e = (uint64_t)blockIdx.x * kSumThreads + threadIdx.x;
+  const uint32_t n = (uint32_t)(e / quads), k = (uint32_t)(e % quads) * 4;
+  if (n >= N) return;
+  const float* p = part + (uint64_t)n * (4 * quads) + k;
+  f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 4
+  for (uint32_t i = 1; i < parts; ++i) v += *reinterpret_cast<const f32x4*>(p + i * part_floats);
+  float* const to = dw + (uint64_t)n * lddw + k;
+  if (k + 4 <= K) {
+    if (accumulate) v += *reinterpret_cast<const f32x4_a4*>(to);
+    *reinterpret_cast<f32x4_a4*>(to) = v;
+  } else {
+#pragma unroll
+    for (uint32_t c = 0; c < 3; ++c)
+      if (k + c < K) to[c] = accumulate ? to[c] + v[c] : v[c];
+  }
+}
 
 namespace {
 
+#ifndef WG_BIG
+#define WG_BIG 24
+#endif
+constexpr uint64_t kWgradLeast = 4;  // blocks of a part
+
+struct WgradPlan {
+  uint32_t side, nt, kt;  // of the tiles
+  Cut cut;
+  uint64_t part_floats;
+};
+WgradPlan wgrad_plan(uint64_t M, uint64_t N, uint64_t K) {
+  WgradPlan p;
+  auto tiles = [&](uint64_t side) { return ((N + side - 1) / side) * ((K + side - 1) / side); };
+  const uint64_t blocks = (M + kWgradRows - 1) / kWgradRows;
+  p.side = tiles(256) * blocks >= WG_BIG * kTileCus ? 256 : 128;
+  p.nt = (uint32_t)((N + p.side - 1) / p.side);
+  p.kt = (uint32_t)((K + p.side - 1) / p.side);
+  // one 256-side workgroup fits a compute unit, two of the others
+  const uint64_t room = p.side == 256 ? kTileCus : 2 * kTileCus;
+  const uint64_t parts = std::min(room / std::max<uint64_t>(1, tiles(p.side)), blocks / kWgradLeast);
+  p.cut = cut_evenly((uint32_t)blocks, (uint32_t)std::max<uint64_t>(1, parts));
+  p.part_floats = N * ((K + 3) / 4 * 4);
+  return p;
+}
+
 template <int KY, int FX>
 void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8_mat& q,
-              const s2r_q8_mat& x, float* dw, uint64_t lddw, bool accumulate, hipStream_t s) {
-  const uint32_t nt = (uint32_t)((N + 255) / 256), kt = (uint32_t)((K + 255) / 256);
-  hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 4, 4>), dim3(nt * kt), dim3(256), 0, s, d, q, x, dw,
-                     lddw, 0, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, (uint32_t)M);
+              const s2r_q8_mat& x, float* dw, uint64_t lddw, bool accumulate, float* workspace,
+              hipStream_t s) {
+  WgradPlan p = wgrad_plan(M, N, K);
+  if (!workspace) p.cut = {1, (uint32_t)((M + kWgradRows - 1) / kWgradRows)};
+  const bool cut = p.cut.parts > 1;
+  const uint32_t grid = p.nt * p.kt * p.cut.parts, rows = p.cut.blocks * kWgradRows;
+  float* const to = cut ? workspace : dw;
+  const uint64_t ld = cut ? (K + 3) / 4 * 4 : lddw;
+  const bool add = accumulate && !cut;
+  trace_mark(s, "k_q8_wgrad");
+  if (p.side == 256)
+    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 4, 4>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
+                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows);
+  else
+    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
+                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows);
+  if (!cut) return;
+  trace_mark(s, "k_q8_wgrad_sum");
+  const uint64_t quads = N * ((K + 3) / 4);
+  hipLaunchKernelGGL(k_q8_wgrad_sum, dim3((uint32_t)((quads + kSumThreads - 1) / kSumThreads)),
+                     dim3(kSumThreads), 0, s, workspace, p.part_floats, p.cut.parts, dw, lddw,
+                     (uint32_t)N, (uint32_t)K, accumulate);
 }
 
 }  // namespace
 
+size_t q8_wgrad_workspace(uint64_t M, uint64_t N, uint64_t K) {
+  const WgradPlan p = wgrad_plan(M, N, K);
+  return p.cut.parts > 1 ? p.cut.parts * p.part_floats * sizeof(float) : 0;
+}
+
 hipError_t launch_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy16,
                            const s2r_q8_mat* dy8, const s2r_q8_mat& x, float* dw, uint64_t lddw,
-                           bool accumulate, void*, hipStream_t s) {
+                           bool accumulate, void* workspace, hipStream_t s) {
   const s2r_mat d = dy16 ? *dy16 : s2r_mat{};
   const s2r_q8_mat q = dy8 ? *dy8 : s2r_q8_mat{};
-  trace_mark(s, "k_q8_wgrad");
-#define S2R_WGRAD(KY, FX) go_wgrad<KY, FX>(M, N, K, d, q, x, dw, lddw, accumulate, s)
+  float* const ws = static_cast<float*>(workspace);
+#define S2R_WGRAD(KY, FX) go_wgrad<KY, FX>(M, N, K, d, q, x, dw, lddw, accumulate, ws, s)
   const int ky = dy16 ? kBf16 : (int)dy8->format;
   if (x.format == S2R_E4M3) {
     if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E4M3);
