@@ -56,11 +56,11 @@ __device__ inline f32x16 mma32(const i32x8& b, const i32x8& a, const f32x16& c, 
 // tile's first blocks arrive while the last ones of this are multiplied and its results leave.
 __device__ inline uint32_t spread(uint32_t p) { return p / 2 % 4 | p / 16 % 2 << 2; }
 
-// 32 x 64 results from LDS: rows m0, m0 + step, ..., columns n0 .. n0 + 63; lane l takes eight
+// ROWS x 64 results from LDS: rows m0, m0 + step, ..., columns n0 .. n0 + 63; lane l takes eight
 // columns of rows l / 8 + 8 k.  They leave through a view that ends with row M - 1; lanes
 // without eight columns aim beyond its end.
-template <int DT>
-__device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[4][2], uint32_t m0, uint32_t step,
+template <int DT, int ROWS>
+__device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[ROWS / 8][2], uint32_t m0, uint32_t step,
                                   uint32_t M, uint32_t n0, uint32_t N) {
   constexpr uint32_t size = elem_bytes<DT>(), kNowhere = 0xffff0000u;
   const uint64_t first = (uint64_t)m0 * c.ld + n0, last = (uint64_t)(M - 1) * c.ld + N;
@@ -69,7 +69,7 @@ __device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[4][2], uint
   const uint32_t ld = step * (uint32_t)c.ld * size;
   const uint32_t at = n0 + n < N ? lane / 8 * ld + n * size : kNowhere;
 #pragma unroll
-  for (uint32_t k = 0; k < 4; ++k) {
+  for (uint32_t k = 0; k < ROWS / 8; ++k) {
     const uint32_t to = n0 + n < N ? at + 8 * k * ld : kNowhere;
     const f32x4 lo = v[k][0], hi = v[k][1];
     if (DT == S2R_F32) {
@@ -83,42 +83,44 @@ __device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[4][2], uint
   }
 }
 
+template <int ROWS>
 __device__ inline void store_turned(const s2r_mat& c, const uint8_t* lds, uint32_t m0, uint32_t step,
                                     uint32_t M, uint32_t n0, uint32_t N) {
   if (m0 >= M || n0 >= N) return;
   const uint32_t lane = threadIdx.x % 64, s = lane % 8 * 2;
-  f32x4 v[4][2];
-#pragma unroll
-  for (uint32_t k = 0; k < 4; ++k) {
-    const uint32_t row = lane / 8 + 8 * k, mix = row % 8 | row / 16 * 8;
-    v[k][0] = *reinterpret_cast<const f32x4*>(lds + row * 256 + (s ^ mix) * 16);
-    v[k][1] = *reinterpret_cast<const f32x4*>(lds + row * 256 + ((s + 1) ^ mix) * 16);
-  }
   if (n0 + 64 > N && N % 8 != 0) {  // a lane may have fewer than eight columns
 #pragma unroll 1
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint32_t m = m0 + step * (lane / 8 + 8 * k), n = n0 + lane % 8 * 8;
-      const f32x4 lo = k == 0 ? v[0][0] : k == 1 ? v[1][0] : k == 2 ? v[2][0] : v[3][0];
-      const f32x4 hi = k == 0 ? v[0][1] : k == 1 ? v[1][1] : k == 2 ? v[2][1] : v[3][1];
+    for (uint32_t row = lane / 8; row < ROWS; row += 8) {
+      const uint32_t m = m0 + step * row, n = n0 + lane % 8 * 8;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(lds + turned(row, s));
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(lds + turned(row, s + 1));
       if (m < M && n < N) store8(c, m, n, N, lo, hi);
     }
-  } else if (c.dtype == S2R_BF16) {
-    store_rows<S2R_BF16>(c, v, m0, step, M, n0, N);
+    return;
+  }
+  f32x4 v[ROWS / 8][2];
+#pragma unroll
+  for (uint32_t k = 0; k < ROWS / 8; ++k) {
+    v[k][0] = *reinterpret_cast<const f32x4*>(lds + turned(lane / 8 + 8 * k, s));
+    v[k][1] = *reinterpret_cast<const f32x4*>(lds + turned(lane / 8 + 8 * k, s + 1));
+  }
+  if (c.dtype == S2R_BF16) {
+    store_rows<S2R_BF16, ROWS>(c, v, m0, step, M, n0, N);
   } else if (c.dtype == S2R_F16) {
-    store_rows<S2R_F16>(c, v, m0, step, M, n0, N);
+    store_rows<S2R_F16, ROWS>(c, v, m0, step, M, n0, N);
   } else {
-    store_rows<S2R_F32>(c, v, m0, step, M, n0, N);
+    store_rows<S2R_F32, ROWS>(c, v, m0, step, M, n0, N);
   }
 }
 
 template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
+__global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm(
     s2r_q8_mat a, s2r_q8_mat b, s2r_mat c, uint64_t part_bytes, uint32_t M, uint32_t N, uint32_t K,
     uint32_t m_tiles, uint32_t n_tiles, uint32_t total, uint32_t part_blocks) {
   constexpr int kWaves = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
   constexpr int kLoadsA = TM / 8 / kWaves, kLoads = (TM + TN) / 8 / kWaves;
   constexpr int kBytes = (TM + TN) * kQ8Block;
-  constexpr int kTurn = 32 * 64 * 4;  // a wave's room for 32 x 64 results
+  constexpr int kTurnRows = kWaves > 4 ? 16 : 32, kTurn = kTurnRows * 64 * 4;  // a wave's results in LDS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBytes + kWaves * kTurn];
 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -288,29 +290,31 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
       sa = sa_next;
       sb = sb_next;
     }
-    // 32 x 64 results at a time turn in LDS, so that whole lines leave; piece s of row p is at
-    // s ^ (p % 8, p / 16)
+    // kTurnRows x 64 results at a time turn in LDS, so that whole lines leave
     const uint32_t m0 = t.row * TM + wm, n0 = t.col * TN + wn;  // of this wave
     if (m0 >= M || n0 >= N) continue;
     uint8_t* const mine = lds + 2 * kBytes + wave * kTurn;
-    const uint32_t mix = r % 8 | r / 16 * 8;
     s2r_mat out = c;
     out.data = static_cast<uint8_t*>(c.data) + t.part * part_bytes;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; j += 2) {
+      for (int j = 0; j < FN; j += 2)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const f32x16& x = acc[i][j + e / 4];
-          const int q = e % 4 * 4;
-          *reinterpret_cast<f32x4*>(mine + r * 256 + ((2 * e + g) ^ mix) * 16) =
-              f32x4{x[q], x[q + 1], x[q + 2], x[q + 3]};
+        for (int h = 0; h < 32 / kTurnRows; ++h) {
+          if (kTurnRows == 32 || r / kTurnRows == h) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const f32x16& x = acc[i][j + e / 4];
+              const int q = e % 4 * 4;
+              *reinterpret_cast<f32x4*>(mine + turned(r % kTurnRows, 2 * e + g)) =
+                  f32x4{x[q], x[q + 1], x[q + 2], x[q + 3]};
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+          store_turned<kTurnRows>(out, mine, m0 + i + FM * kTurnRows * h, FM, M, n0 + 32 * j, N);
+          __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
-        store_turned(out, mine, m0 + i, FM, M, n0 + 32 * j, N);
-        __builtin_amdgcn_wave_barrier();
-      }
   }
   drain_and_sync();
 }

@@ -75,8 +75,13 @@ __device__ inline TileAt tile_at(uint32_t b, uint32_t rows, uint32_t cols, uint3
   return t;
 }
 
-// 32 x 64 fp32 results from LDS, laid out as the products leave them (16-byte piece s of row p
-// at s ^ (p % 8, p / 16)), to rows n0 .., columns k0 .. of dw, or added to what is there.  Four
+// Results turn in LDS, 64 fp32 columns to a row: where 16-byte piece s of row p lies.  The lanes
+// that write together, one piece of 16 rows, and those that read a row meet every bank once.
+__device__ inline uint32_t turned(uint32_t p, uint32_t s) {
+  return p * 256 + (s ^ (p % 8 | (p / 8 ^ p / 16) % 2 * 8)) * 16;
+}
+
+// 32 x 64 results from LDS to rows n0 .., columns k0 .. of dw, or added to what is there.  Four
 // columns per lane, 16 lanes a row; dw is only known to be 4-byte aligned.
 __device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, uint32_t n0, uint32_t N,
                                   uint32_t k0, uint32_t K, bool accumulate) {
@@ -86,8 +91,7 @@ __device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, ui
   f32x4 v[8];
 #pragma unroll
   for (uint32_t e = 0; e < 8; ++e) {
-    const uint32_t row = lane / 16 + 4 * e, mix = row % 8 | row / 16 * 8;
-    v[e] = *reinterpret_cast<const f32x4*>(lds + row * 256 + (s ^ mix) * 16);
+    v[e] = *reinterpret_cast<const f32x4*>(lds + turned(lane / 16 + 4 * e, s));
   }
   float* const at = dw + (uint64_t)(n0 + lane / 16) * ld + k;
   if (n0 + 32 <= N && k0 + 64 <= K) {

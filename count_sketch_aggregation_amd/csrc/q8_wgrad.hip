@@ -13,22 +13,14 @@ namespace s2r {
 constexpr int kWgradRows = 64;  // rows m of a block of the sum
 constexpr int kBf16 = 2;        // kind of an operand that is bf16 already (else its q8 format)
 
-// 16 codes to bf16: exact, as a scale is a power of two and a stored value a normal bf16.
+// Four codes to bf16: exact, as a scale is a power of two and a stored value a normal bf16.
 template <int FMT>
-__device__ inline void to_bf16(u32x4 q, float scale, u32x4& lo, u32x4& hi) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t a, b;
-    if (FMT == S2R_E4M3) {
-      a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[w], scale, false));
-      b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[w], scale, true));
-    } else {
-      a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[w], scale, false));
-      b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[w], scale, true));
-    }
-    (w < 2 ? lo : hi)[w % 2 * 2] = a;
-    (w < 2 ? lo : hi)[w % 2 * 2 + 1] = b;
-  }
+__device__ inline u32x2 to_bf16(uint32_t q, float scale) {
+  if (FMT == S2R_E4M3)
+    return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, true))};
+  return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, false)),
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, true))};
 }
 
 // An operand on its way to LDS, a block of 64 rows x COLS columns at a time, bf16 there: 64-byte
@@ -47,8 +39,10 @@ struct Feed {
   uint32_t wave, row, last;
   const uint8_t* scale;
   uint32_t to;                // LDS place of this lane's first codes
-  u32x4 code[kLoads];
-  uint32_t sb[kLoads];
+  static constexpr int kUnits = kDirect ? 0 : 4 * kLoads;  // four codes of every lane each
+  u32x4 next[kLoads], code[kLoads];  // a block's codes: on their way, and being decoded
+  uint32_t next_sb[kLoads], sb[kLoads];
+  u32x4 half;
 
   __device__ void start(const s2r_mat& m, const s2r_q8_mat& q, uint32_t c0, uint32_t cols,
                         uint32_t first, uint32_t end, uint32_t w) {
@@ -81,8 +75,8 @@ struct Feed {
   // The compiler would have every transposing load of LDS wait for every load that is on its
   // way there: it is not told of these, and the loop waits for them itself.  Nothing comes back
   // to a register; the pause covers scalar registers that a vector instruction has just written.
-  __device__ void load(uint8_t* lds, u32x4 v, int j) const {
-    const uint32_t to = (uint32_t)(uintptr_t)(lds_void*)(lds + (wave * kLoads + j) * 1024);
+  __device__ void load(uint32_t lds, u32x4 v, int j) const {
+    const uint32_t to = lds + (wave * kLoads + j) * 1024;
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at[j]), "s"(v) : "memory");
   }
@@ -92,27 +86,44 @@ struct Feed {
                  (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32) & 0xffffu),
                  (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
   }
-  // codes of the next block, with their scales (of a row beyond the end: any, its codes are 0)
+  // codes of the next block, with their scales (of a row beyond the end: any finite one, its codes
+  // are 0; kWgradRows and kRows are multiples of 4, and so is `first`)
   __device__ void fetch() {
     const auto v = view();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      code[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, at[j], 0, 0));
-      sb[j] = scale[min(row + j * kRows, last)];
+      next[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, at[j], 0, 0));
+      next_sb[j] = *reinterpret_cast<const uint32_t*>(scale + min(row + j * kRows, last) / 4 * 4);
     }
     row += kWgradRows;
   }
-  // Piece j decoded.  Half of the lanes write their upper half first: together the lanes of a
-  // write then meet every bank.
-  __device__ void decode(uint8_t* lds, int j) const {
+  // The fetched codes become those that are decoded: moved here, where they are known to have
+  // come, and not by the compiler further up.
+  __device__ void take() {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t c;
+        asm volatile("v_mov_b32 %0, %1" : "=v"(c) : "v"(next[j][w]));
+        code[j][w] = c;
+      }
+      uint32_t b;  // of four rows; this lane's is the same one in every block
+      asm volatile("v_mov_b32 %0, %1" : "=v"(b) : "v"(next_sb[j]));
+      sb[j] = min(b >> row % 4 * 8 & 0xff, 254u) << 23;
+    }
+  }
+  // Unit u decoded.  Half of the lanes write their upper 16 bytes first: together the lanes of
+  // a write then meet every bank.
+  __device__ void decode(uint8_t* lds, int u) {
     const bool swap = threadIdx.x / 8 % 2;
-    const u32x4 c = code[j];
-    u32x4 lo, hi;
-    to_bf16 < KIND == S2R_E5M2 ? S2R_E5M2 : S2R_E4M3 > (u32x4{swap ? c[2] : c[0], swap ? c[3] : c[1],
-            swap ? c[0] : c[2], swap ? c[1] : c[3]}, scale_value(sb[j]), lo, hi);
-    uint8_t* p = lds + to + j * (kRows * kRowBytes);
-    *reinterpret_cast<u32x4*>(p + (swap ? 16 : 0)) = lo;
-    *reinterpret_cast<u32x4*>(p + (swap ? 0 : 16)) = hi;
+    const int j = u / 4, w = u % 4;
+    const u32x2 v = to_bf16<KIND == S2R_E5M2 ? S2R_E5M2 : S2R_E4M3>(
+        swap ? code[j][w ^ 2] : code[j][w], __uint_as_float(sb[j]));
+    half[w % 2 * 2] = v[0];
+    half[w % 2 * 2 + 1] = v[1];
+    if (w % 2)
+      *reinterpret_cast<u32x4*>(lds + to + j * (kRows * kRowBytes) + ((w == 3) != swap ? 16 : 0)) = half;
   }
 };
 
@@ -121,10 +132,10 @@ struct Feed {
 // memory has columns side by side: LDS is read with the transposing load, four rows of 16
 // columns to a lane each.  LDS holds two blocks of both operands; the fragments of a step are
 // read while the step before is multiplied, so a block's LDS is free before its last step:
-// there the block after the next begins to arrive, and its codes, which came to registers
-// meanwhile, are decoded.
+// there the block after the next begins to arrive.  Codes come to registers a block before, and
+// are decoded all along the next one's steps.
 template <int KY, int FX, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
+__global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgrad(
     s2r_mat dy16, s2r_q8_mat dy8, s2r_q8_mat xq, float* dw, uint64_t lddw, uint64_t part_floats,
     uint32_t M, uint32_t N, uint32_t K, bool accumulate, uint32_t n_tiles, uint32_t k_tiles,
     uint32_t part_rows) {
@@ -170,13 +181,13 @@ __global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
     X x;
     y.start(dy16, dy8, n0, N, m0, m1, wave);
     x.start(dy16, xq, k0, K, m0, m1, wave);
-    uint8_t *here = lds, *there = lds + (Y::kBytes + X::kBytes);
-    auto load_y = [&](uint8_t* to, int e, int of) {  // share e of a block
-      if (!Y::kDirect) return;
+    constexpr uint32_t kBytes = Y::kBytes + X::kBytes;
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void*)lds;
+    uint32_t here = 0, there = kBytes;
+    auto load_y = [&](uint32_t to, int e, int of) {  // share e of a block
       const u32x4 v = y.words();
 #pragma unroll
-      for (int j = e * Y::kLoads / of; j < (e + 1) * Y::kLoads / of; ++j) y.load(to, v, j);
-      if (e == of - 1) y.advance();
+      for (int j = e * Y::kLoads / of; j < (e + 1) * Y::kLoads / of; ++j) y.load(lds_at + to, v, j);
     };
     auto fetch = [&] {
       x.fetch();
@@ -186,36 +197,50 @@ __global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
         y.advance();
       }
     };
-    constexpr int kPieces = X::kLoads + (Y::kDirect ? 0 : Y::kLoads);
-    auto decode = [&](uint8_t* to, int e, int of) {
+    auto take = [&] {
+      x.take();
+      if (!Y::kDirect) y.take();
+    };
+    constexpr int kUnits = X::kUnits + Y::kUnits, kSlots = 4 * kMma;
+    auto decode = [&](uint32_t to, int first, int end) {
 #pragma unroll
-      for (int j = e * kPieces / of; j < (e + 1) * kPieces / of; ++j) {
-        if (j < X::kLoads) x.decode(to + Y::kBytes, j);
-        else if (!Y::kDirect) y.decode(to, j - X::kLoads);
+      for (int u = first; u < end; ++u) {
+        if (u < X::kUnits) x.decode(lds + to + Y::kBytes, u);
+        else if (!Y::kDirect) y.decode(lds + to, u - X::kUnits);
       }
     };
     fetch();
-    load_y(here, 0, 1);
-    decode(here, 0, 1);
-    fetch();
-    load_y(there, 0, 1);
-    decode(there, 0, 1);
-    fetch();
+    if (Y::kDirect) {
+      load_y(here, 0, 1);
+      y.advance();
+      load_y(there, 0, 1);
+      y.advance();
+    }
     drain_and_sync();
+    take();
+    fetch();
+    decode(here, 0, kUnits);
+    drain_and_sync();
+    take();
+    fetch();
+    decode(there, 0, kUnits / 4);
     Frags f0, f1;
 #pragma unroll
-    for (int e = 0; e < kReads; ++e) read(f0, here, here + Y::kBytes, 0, e);
+    for (int e = 0; e < kReads; ++e) read(f0, lds + here, lds + here + Y::kBytes, 0, e);
 
     auto multiply = [&](const Frags& f, int e) {
       acc[e / FN][e % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[e % FN], f.y[e / FN], acc[e / FN][e % FN], 0, 0, 0);
     };
+    // step s of a block: the next one's fragments are read, the next block's codes decoded
     auto step = [&](const Frags& f, Frags& next, int s) {
 #pragma unroll
       for (int e = 0; e < kMma; ++e) {
         multiply(f, e);
 #pragma unroll
         for (int i = e * kReads / kMma; i < (e + 1) * kReads / kMma; ++i)
-          read(next, here, here + Y::kBytes, s + 1, i);
+          read(next, lds + here, lds + here + Y::kBytes, s + 1, i);
+        const int slot = (s + 1) * kMma + e;
+        decode(there, slot * kUnits / kSlots, (slot + 1) * kUnits / kSlots);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -224,18 +249,20 @@ __global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
       step(f1, f0, 1);
       step(f0, f1, 2);
       drain_and_sync();  // the next block is there, codes are in registers, this LDS is free
+      take();
+      fetch();
 #pragma unroll
       for (int e = 0; e < kMma; ++e) {
         multiply(f1, e);
 #pragma unroll
         for (int i = e * kReads / kMma; i < (e + 1) * kReads / kMma; ++i)
-          read(f0, there, there + Y::kBytes, 0, i);
-        load_y(here, e, kMma);
-        decode(here, e, kMma);
+          read(f0, lds + there, lds + there + Y::kBytes, 0, i);
+        if (Y::kDirect) load_y(here, e, kMma);
+        decode(here, e * kUnits / kSlots, (e + 1) * kUnits / kSlots);
         __builtin_amdgcn_sched_barrier(0);
       }
-      fetch();
-      uint8_t* const t = here;
+      if (Y::kDirect) y.advance();
+      const uint32_t t = here;
       here = there;
       there = t;
     }
@@ -247,7 +274,6 @@ __global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
   constexpr int kTurn = 32 * 64 * 4;
   static_assert(kWaves * kTurn <= (int)sizeof(lds), "");
   uint8_t* const mine = lds + wave * kTurn;
-  const uint32_t mix = r % 8 | r / 16 * 8;
   float* const out = dw + t.part * part_floats;
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -257,7 +283,7 @@ __global__ __launch_bounds__(64 * WM * WN, FM == 4 ? 1 : 2) void k_q8_wgrad(
       for (int e = 0; e < 8; ++e) {
         const f32x16& v = acc[i][j + e / 4];
         const int w = e % 4 * 4;
-        *reinterpret_cast<f32x4*>(mine + r * 256 + ((2 * e + g) ^ mix) * 16) = f32x4{v[w], v[w + 1], v[w + 2], v[w + 3]};
+        *reinterpret_cast<f32x4*>(mine + turned(r, 2 * e + g)) = f32x4{v[w], v[w + 1], v[w + 2], v[w + 3]};
       }
       __builtin_amdgcn_wave_barrier();
       add_turned(out, lddw, mine, n0 + wm + 32 * i, N, k0 + wn + 32 * j, K, accumulate);
@@ -331,7 +357,7 @@ void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8
   const bool add = accumulate && !cut;
   trace_mark(s, "k_q8_wgrad");
   if (p.side == 256)
-    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 4, 4>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
+    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 4, 4, 2>), dim3(grid), dim3(512), 0, s, d, q, x, to, ld,
                        p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows);
   else
     hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
