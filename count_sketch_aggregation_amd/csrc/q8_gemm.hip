@@ -3,6 +3,9 @@
 // The scaled matrix instruction multiplies both operands by their scales itself, so one fp32
 // accumulator runs over the whole sum.  The first operand is B, so that a lane's results
 // are consecutive columns of C.
+#include <algorithm>
+#include <type_traits>
+
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
@@ -248,8 +251,8 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
     auto multiply = [&](const Frags& f, int e) {
       acc[e / FN][e % FN] = mma32<FA, FB>(f.b[e % FN], f.a[e / FN], acc[e / FN][e % FN], sb, sa, e / FN);
     };
-    for (uint32_t block = b0; block < b1; ++block) {
-      if (TAIL) clear_tail(f0, (int)(K - block * kQ8Block));
+    auto run = [&](auto clear, uint32_t block) {  // one block, without the codes at or beyond K
+      if (clear) clear_tail(f0, (int)(K - block * kQ8Block));
 #pragma unroll
       for (int e = 0; e < kRead; ++e) {
         multiply(f0, e);
@@ -275,7 +278,7 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
       asm volatile("v_mov_b32 %0, %1" : "=v"(sa_next) : "v"(sa_ahead));
       asm volatile("v_mov_b32 %0, %1" : "=v"(sb_next) : "v"(sb_ahead));
       load_scales(sa_ahead, sb_ahead);
-      if (TAIL) clear_tail(f1, (int)(K - block * kQ8Block) - 64);
+      if (clear) clear_tail(f1, (int)(K - block * kQ8Block) - 64);
 #pragma unroll
       for (int e = 0; e < kMma; ++e) {
         multiply(f1, e);
@@ -289,7 +292,10 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
       there = x;
       sa = sa_next;
       sb = sb_next;
-    }
+    };
+    const uint32_t whole = TAIL && b1 == blocks ? b1 - 1 : b1;
+    for (uint32_t block = b0; block < whole; ++block) run(std::false_type(), block);
+    if (TAIL && b1 == blocks) run(std::true_type(), b1 - 1);
     // kTurnRows x 64 results at a time turn in LDS, so that whole lines leave
     const uint32_t m0 = t.row * TM + wm, n0 = t.col * TN + wn;  // of this wave
     if (m0 >= M || n0 >= N) continue;
@@ -329,6 +335,7 @@ __device__ inline f32x4 mma(const i32x8& b, const i32x8& a, const f32x4& c, uint
 // Up to 16 FM rows of A: the rows of B are read once, straight into registers, and bound the
 // call.  A workgroup takes 16 of them and cuts the sum among its waves, block by block in
 // turn; the partial sums meet in LDS and are added in the order of the waves.
+constexpr uint64_t kFewRows = 64;
 constexpr int kFewBatch = 2;  // blocks of the sum a wave has in flight
 
 __device__ inline i32x8 load_frag(const uint8_t* row, uint32_t k, uint32_t K) {
@@ -388,15 +395,62 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
   }
 }
 
-size_t q8_gemm_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
+// The parts of a sum, added in their order.
+constexpr int kSumThreads = 256;
+__global__ __launch_bounds__(kSumThreads) void k_q8_gemm_sum(const float* __restrict__ part,
+                                                             uint64_t part_floats, uint32_t parts,
+                                                             s2r_mat c, uint32_t M, uint32_t N) {
+  const uint32_t quads = (N + 3) / 4;
+  const uint64_t e = (uint64_t)blockIdx.x * kSumThreads + threadIdx.x;
+  const uint32_t m = (uint32_t)(e / quads), n = (uint32_t)(e % quads) * 4;
+  if (m >= M) return;
+  const float* p = part + (uint64_t)m * (4 * quads) + n;
+  f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 4
+  for (uint32_t i = 1; i < parts; ++i) v += *reinterpret_cast<const f32x4*>(p + i * part_floats);
+  store4(c, m, n, N, v);
+}
 
 namespace {
 
+// Tiles and parts of the sum with the least estimated time, in nanoseconds.  A tile of 256 x 256
+// takes 1350 for a block of the sum and 8000 to begin and to leave, one of 256 x 128 900 and
+// 6000, one of 128 x 128 680 and 5000 (measured at K = 4096 with one tile on every compute
+// unit), and the compute units take them in rounds.  Parts are written and read again, at 4
+// bytes a picosecond, by a launch of 3000.
+struct GemmPlan {
+  uint32_t tm, tn, mt, nt, blocks;
+  Cut cut;
+};
+GemmPlan gemm_plan(uint64_t M, uint64_t N, uint64_t K) {
+  static constexpr uint32_t kTiles[][4] = {
+      {256, 256, 1350, 8000}, {256, 128, 900, 6000}, {128, 128, 680, 5000}};
+  const uint32_t blocks = (uint32_t)((K + kQ8Block - 1) / kQ8Block);
+  GemmPlan best = {};
+  uint64_t least = ~0ull;
+  for (const auto& t : kTiles) {
+    GemmPlan p = {t[0], t[1], (uint32_t)((M + t[0] - 1) / t[0]), (uint32_t)((N + t[1] - 1) / t[1]),
+                  blocks, {1, blocks}};
+    const uint64_t tiles = (uint64_t)p.mt * p.nt;
+    for (uint32_t parts = 1; parts <= 16; ++parts) {
+      p.cut = cut_evenly(blocks, parts);
+      if (parts > 1 && (p.cut.parts != parts || p.cut.blocks < 2 || blocks % p.cut.blocks == 1 ||
+                        tiles * parts > kTileCus))
+        continue;  // as few parts give the same, or one has a single block beside longer ones
+      const uint64_t rounds = (tiles * parts + kTileCus - 1) / kTileCus;
+      uint64_t ns = rounds * ((uint64_t)p.cut.blocks * t[2] + t[3]);
+      if (parts > 1) ns += 3000 + M * N * 4 * (2 * parts + 1) / 4000;
+      if (ns < least) least = ns, best = p;
+    }
+  }
+  return best;
+}
+
 template <int FA, int FB>
 void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_q8_mat& b,
-             const s2r_mat& c, hipStream_t s) {
+             const s2r_mat& c, void* workspace, hipStream_t s) {
   const uint32_t m = (uint32_t)M, n = (uint32_t)N, k = (uint32_t)K;
-  if (M <= 64) {
+  if (M <= kFewRows) {
     trace_mark(s, "k_q8_gemm_few");
     const dim3 grid((n + 15) / 16);
     if (M <= 16)
@@ -408,34 +462,54 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
     return;
   }
   trace_mark(s, "k_q8_gemm");
-  const uint32_t blocks = (k + kQ8Block - 1) / kQ8Block;
-#ifdef V2
-  const uint32_t mt = (m + 255) / 256, nt = (n + 127) / 128;
-  constexpr int FN = 2;
-#else
-  const uint32_t mt = (m + 255) / 256, nt = (n + 255) / 256;
-  constexpr int FN = 4;
-#endif
-  const uint32_t total = mt * nt;
-  const dim3 grid(min(total, kTileCus));
-  if (k % kQ8Block == 0)
-    hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, 4, FN, false>), grid, dim3(256), 0, s, a, b, c, 0,
-                     m, n, k, mt, nt, total, blocks);
-  else
-    hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, 4, FN, true>), grid, dim3(256), 0, s, a, b, c, 0,
-                     m, n, k, mt, nt, total, blocks);
+  GemmPlan p = gemm_plan(M, N, K);
+  if (!workspace) p.cut = {1, p.blocks};
+  const bool cut = p.cut.parts > 1;
+  s2r_mat out = c;
+  if (cut) out = {workspace, (N + 3) / 4 * 4, S2R_F32};
+  const uint64_t part_bytes = M * out.ld * sizeof(float);
+  const uint32_t total = p.mt * p.nt * p.cut.parts;
+  const dim3 grid(std::min(total, kTileCus));
+#define S2R_TILE(FM, FN, TAIL)                                                                    \
+  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, FM, FN, TAIL>), grid, dim3(256), 0, s, a, b, out,    \
+                     part_bytes, m, n, k, p.mt, p.nt, total, p.cut.blocks)
+  trace_mark(s, "k_q8_gemm");
+  if (p.tm == 256 && p.tn == 256) {
+    if (k % kQ8Block == 0) S2R_TILE(4, 4, false);
+    else S2R_TILE(4, 4, true);
+  } else if (p.tm == 256) {
+    if (k % kQ8Block == 0) S2R_TILE(4, 2, false);
+    else S2R_TILE(4, 2, true);
+  } else {
+    if (k % kQ8Block == 0) S2R_TILE(2, 2, false);
+    else S2R_TILE(2, 2, true);
+  }
+#undef S2R_TILE
+  if (!cut) return;
+  trace_mark(s, "k_q8_gemm_sum");
+  const uint64_t quads = M * ((N + 3) / 4);
+  hipLaunchKernelGGL(k_q8_gemm_sum, dim3((uint32_t)((quads + kSumThreads - 1) / kSumThreads)),
+                     dim3(kSumThreads), 0, s, static_cast<const float*>(workspace), part_bytes / 4,
+                     p.cut.parts, c, m, n);
 }
 
 }  // namespace
 
+size_t q8_gemm_workspace(uint64_t M, uint64_t N, uint64_t K) {
+  if (M <= kFewRows) return 0;
+  const GemmPlan p = gemm_plan(M, N, K);
+  return p.cut.parts > 1 ? p.cut.parts * M * ((N + 3) / 4 * 4) * sizeof(float) : 0;
+}
+
 hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a,
-                          const s2r_q8_mat& b, const s2r_mat& c, void*, hipStream_t s) {
+                          const s2r_q8_mat& b, const s2r_mat& c, void* workspace,
+                          hipStream_t s) {
   if (a.format == S2R_E4M3) {
-    if (b.format == S2R_E4M3) go_gemm<S2R_E4M3, S2R_E4M3>(M, N, K, a, b, c, s);
-    else go_gemm<S2R_E4M3, S2R_E5M2>(M, N, K, a, b, c, s);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E4M3, S2R_E4M3>(M, N, K, a, b, c, workspace, s);
+    else go_gemm<S2R_E4M3, S2R_E5M2>(M, N, K, a, b, c, workspace, s);
   } else {
-    if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, s);
-    else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, s);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, workspace, s);
+    else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, workspace, s);
   }
   return hipGetLastError();
 }

@@ -319,9 +319,10 @@ __global__ __launch_bounds__(kSumThreads) void k_q8_wgrad_sum(const float* __res
 
 namespace {
 
-#ifndef WG_BIG
-#define WG_BIG 24
-#endif
+// Tiles of 256 x 256 where each compute unit gets kWgradDeep blocks of 64 rows or more of them,
+// as it holds one such workgroup; tiles of 128 x 128 otherwise, two of which fit one.  Measured: 8192 x
+// 2048 x 2048 (32 blocks) 88 us in tiles of 256, 95 in tiles of 128; 4096 x 2048 x 2048 (16) 60 and 56.
+constexpr uint64_t kWgradDeep = 24;
 constexpr uint64_t kWgradLeast = 4;  // blocks of a part
 
 struct WgradPlan {
@@ -333,7 +334,7 @@ WgradPlan wgrad_plan(uint64_t M, uint64_t N, uint64_t K) {
   WgradPlan p;
   auto tiles = [&](uint64_t side) { return ((N + side - 1) / side) * ((K + side - 1) / side); };
   const uint64_t blocks = (M + kWgradRows - 1) / kWgradRows;
-  p.side = tiles(256) * blocks >= WG_BIG * kTileCus ? 256 : 128;
+  p.side = tiles(256) * blocks >= kWgradDeep * kTileCus ? 256 : 128;
   p.nt = (uint32_t)((N + p.side - 1) / p.side);
   p.kt = (uint32_t)((K + p.side - 1) / p.side);
   // one 256-side workgroup fits a compute unit, two of the others

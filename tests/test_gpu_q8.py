@@ -245,6 +245,18 @@ def test_gemm_keeps_non_finite_values_in_their_row(M):
     assert torch.equal(got[3:], va[3:] @ vb.t())
 
 
+@pytest.mark.parametrize("K", [100, 128, 300, 512])
+def test_gemm_of_many_tiles(K):
+    """More tiles than compute units, of one block of the sum and of several, whole and not."""
+    M, N = 4500, 4300
+    gp.say(f"gemm many tiles {M}x{N}x{K}")
+    a, va = integers(M, K, "e4m3", 1)
+    b, vb = integers(N, K, "e4m3", 2, True)
+    want = va.float() @ vb.float().t()  # exact: multiples of 1/4 below 2^22
+    assert torch.equal(gemm(M, N, K, a, b, "f32", True), want)
+    assert torch.equal(gemm(M, N, K, a, b, "bf16", False), want.bfloat16())
+
+
 def test_empty_sums():
     gp.say("empty sums")
     q = s2r.s2r_q8_mat(None, 16, None, 64, 0)
@@ -322,6 +334,23 @@ def test_wgrad_on_ordinary_values(M, N, K, kind):
     for with_ws in (False, True):
         got = wgrad(M, N, K, dy, x, with_ws=with_ws)
         assert bool(((got - want).abs() <= M * 2.0 ** -23 * mass).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(6200, 2100, 2100), (1700, 4100, 4200)])
+def test_wgrad_of_large_tiles(M, N, K, kind):
+    """Sizes where the larger tiles are taken: a cut sum, and more tiles than compute units."""
+    gp.say(f"wgrad large tiles {M}x{N}x{K} {kind}")
+    if kind == "bf16":
+        vy = torch.randint(-3, 4, (M, N), generator=_gen(7)).double()
+        dy = s2r.mat(wide(M, N, "bf16", x=vy)[:, :N])
+    else:
+        dy, vy = integers(M, N, kind, 7)
+    x, vx = integers(M, K, "e4m3", 8)
+    want = vy.float().t() @ vx.float()  # exact: multiples of 1/4 below 2^22
+    assert torch.equal(wgrad(M, N, K, dy, x).float(), want)
+    dw0 = torch.randint(-50, 51, (N, K), generator=_gen(9)).double()
+    assert torch.equal(wgrad(M, N, K, dy, x, dw0, lddw=K + 3, off=3).float(), want + dw0.float())
 
 
 def test_wgrad_scales_along_the_sum():
