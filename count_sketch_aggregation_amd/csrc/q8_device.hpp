@@ -14,6 +14,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -184,25 +186,27 @@ __device__ inline uint32_t scale_byte(uint32_t amax) {
 }
 
 __device__ inline float scale_value(uint32_t b) { return __uint_as_float(b << 23); }
-__device__ inline float scale_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
 __device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Magnitude bits of the largest finite of 16 values (as integers fp32 magnitudes order as
-// their values; infinities and NaN are at or above 0x7f800000).
+// their values).  The maximum passes over NaN; the instruction takes magnitudes by itself, which
+// the compiler does not use where a value may be a signalling NaN.
 __device__ inline uint32_t amax16(const float (&x)[16]) {
-  uint32_t m = 0;
+  float m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = umax(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  if (m >= 0x7f800000u) {  // rare: once more, without the non-finite ones
-    m = 0;
+  for (int i = 0; i < 16; i += 2)
+    asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(m) : "v"(m), "v"(x[i]), "v"(x[i + 1]));
+  uint32_t most = __float_as_uint(m);
+  if (most >= 0x7f800000u) {  // rare: once more, without the infinities
+    most = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-      m = umax(m, b >= 0x7f800000u ? 0u : b);
+      most = umax(most, b >= 0x7f800000u ? 0u : b);
     }
   }
-  return m;
+  return most;
 }
 
 // Maximum over aligned groups of 8 lanes (a 128-element block at 16 elements per lane): two
@@ -215,49 +219,53 @@ __device__ inline uint32_t max_over_8(uint32_t v) {
 }
 
 // ---- codes --------------------------------------------------------------------------------
-// Four values to four codes: the product with a power of two is exact (or far below the
-// format's least code), the conversion rounds to nearest even and cannot overflow, because
+// Four values to four codes: the conversion divides by the scale (a power of two: exact, or far
+// below the format's least code), rounds to nearest even and cannot overflow, because
 // the block's scale covers its largest finite value; infinities and NaN convert as the
 // format has them.
 template <int FMT>
-__device__ inline uint32_t encode4(float a, float b, float c, float d, float inv) {
-  int v = 0;
+__device__ inline uint32_t encode4(float a, float b, float c, float d, float scale) {
+  s16x2 v = {};
   if (FMT == S2R_E4M3) {
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, v, false);
-    v = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, v, true);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, a, b, scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true);
   } else {
-    v = __builtin_amdgcn_cvt_pk_bf8_f32(a * inv, b * inv, v, false);
-    v = __builtin_amdgcn_cvt_pk_bf8_f32(c * inv, d * inv, v, true);
+    v = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(v, a, b, scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(v, c, d, scale, true);
   }
-  return (uint32_t)v;
+  return __builtin_bit_cast(uint32_t, v);
 }
 
 template <int FMT>
-__device__ inline u32x4 encode16(const float (&x)[16], float inv) {
+__device__ inline u32x4 encode16(const float (&x)[16], float scale) {
   u32x4 q;
 #pragma unroll
   for (int w = 0; w < 4; ++w)
-    q[w] = encode4<FMT>(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3], inv);
+    q[w] = encode4<FMT>(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3], scale);
   return q;
+}
+
+// Four codes to four values, exact.
+template <int FMT>
+__device__ inline f32x4 decode4(uint32_t q, float scale) {
+  f32x2 lo, hi;
+  if (FMT == S2R_E4M3) {
+    lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, scale, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, scale, true);
+  } else {
+    lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(q, scale, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(q, scale, true);
+  }
+  return {lo[0], lo[1], hi[0], hi[1]};
 }
 
 template <int FMT>
 __device__ inline void decode16(u32x4 q, float scale, float (&x)[16]) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    f32x2 lo, hi;
-    if (FMT == S2R_E4M3) {
-      lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[w], false);
-      hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[w], true);
-    } else {
-      lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)q[w], false);
-      hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)q[w], true);
-    }
-    x[4 * w] = lo[0] * scale;
-    x[4 * w + 1] = lo[1] * scale;
-    x[4 * w + 2] = hi[0] * scale;
-    x[4 * w + 3] = hi[1] * scale;
+    const f32x4 v = decode4<FMT>(q[w], scale);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * w + e] = v[e];
   }
 }
 

@@ -19,7 +19,11 @@ constexpr int kGluThreads = 256;
 constexpr int kGluRows = kGluThreads / 8;
 constexpr int kGluBlocks = 2;  // blocks of 128 columns per workgroup: two or three streams each
 
-__device__ inline float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// The hardware's 2^x and reciprocal, each within a unit in the last place: what follows is
+// rounded to 8 or 16 bits.
+__device__ inline float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+}
 
 template <int ACT>
 __device__ inline float act_value(float g) {
@@ -38,7 +42,7 @@ __device__ inline void act_both(float g, float& a, float& d) {
   } else if (ACT == S2R_ACT_GELU) {
     const float c = 0.5f + 0.5f * erff(g * 0.70710678118654752f);
     a = g * c;
-    d = c + g * (expf(-0.5f * g * g) * 0.39894228040143268f);
+    d = c + g * (__builtin_amdgcn_exp2f(-0.72134752044448170f * g * g) * 0.39894228040143268f);
   } else {
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float s = sigmoid(z2);
@@ -55,10 +59,10 @@ __device__ inline void put8(const s2r_q8_mat& o, uint32_t m, uint32_t c, uint32_
   u32x4 code;
   if (o.format == S2R_E4M3) {
     sb = scale_byte<S2R_E4M3>(am);
-    code = encode16<S2R_E4M3>(v, scale_inverse(sb));
+    code = encode16<S2R_E4M3>(v, scale_value(sb));
   } else {
     sb = scale_byte<S2R_E5M2>(am);
-    code = encode16<S2R_E5M2>(v, scale_inverse(sb));
+    code = encode16<S2R_E5M2>(v, scale_value(sb));
   }
   if (c >= F) return;
   store_codes16(o.q + (uint64_t)m * o.ld, c, F, code);

@@ -33,35 +33,57 @@ __global__ __launch_bounds__(kStoreThreads) void k_q8_save(
     float v[16];
     unpack16<DT>(r[b], v);
     const uint32_t sb = scale_byte<FMT>(max_over_8(amax16(v)));
-    if (c < K) store_codes16(qrow, c, K, encode16<FMT>(v, scale_inverse(sb)));
+    if (c < K) store_codes16(qrow, c, K, encode16<FMT>(v, scale_value(sb)));
     if (threadIdx.x % 8 == 0 && c < K) scale[(uint64_t)(c / kQ8Block) * lds + m] = (uint8_t)sb;
   }
 }
 
+// A lane takes the codes of one 16-byte piece of x, a wave 64 pieces of a row: what is written, two
+// to four times what is read, leaves as whole lines.
+constexpr int kLoadRows = 4;  // of a wave
 template <int DT, int FMT>
 __global__ __launch_bounds__(kStoreThreads) void k_q8_load(
     const uint8_t* __restrict__ q, uint64_t ldq, const uint8_t* __restrict__ scale, uint64_t lds,
     void* __restrict__ x, uint64_t ldx, uint32_t M, uint32_t K, uint32_t col_tiles) {
+  using E = typename ElemT<DT>::type;
+  constexpr uint32_t kPer = 16 / elem_bytes<DT>();
   const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
-  const uint32_t m = rt * kStoreRows + threadIdx.x / 8;
-  if (m >= M) return;
-  const uint32_t c0 = ct * (kStoreBlocks * kQ8Block) + (threadIdx.x % 8) * 16;
-  const uint8_t* qrow = q + (uint64_t)m * ldq;
-  auto* row = static_cast<typename ElemT<DT>::type*>(x) + (uint64_t)m * ldx;
-  u32x4 r[kStoreBlocks];
-  uint32_t sb[kStoreBlocks];
+  const uint32_t m0 = (rt * (kStoreThreads / 64) + threadIdx.x / 64) * kLoadRows;
+  const uint32_t c = (ct * 64 + threadIdx.x % 64) * kPer;
+  if (c >= K) return;
+  uint32_t code[kLoadRows][kPer / 4], sb[kLoadRows];
 #pragma unroll
-  for (int b = 0; b < kStoreBlocks; ++b) {
-    const uint32_t c = c0 + b * kQ8Block;
-    r[b] = load_codes16(qrow, c, K);
-    sb[b] = c < K ? scale[(uint64_t)(c / kQ8Block) * lds + m] : 127;
+  for (int i = 0; i < kLoadRows; ++i) {
+    const uint32_t m = min(m0 + i, M - 1);
+    const uint8_t* at = q + (uint64_t)m * ldq + c;
+    if (kPer == 8) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(at);
+      code[i][0] = v[0], code[i][kPer / 4 - 1] = v[1];
+    } else {
+      code[i][0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+    sb[i] = scale[(uint64_t)(c / kQ8Block) * lds + m];
   }
 #pragma unroll
-  for (int b = 0; b < kStoreBlocks; ++b) {
-    const uint32_t c = c0 + b * kQ8Block;
-    float v[16];
-    decode16<FMT>(r[b], scale_value(sb[b]), v);
-    if (c < K) store16<DT>(row, c, K, v);
+  for (int i = 0; i < kLoadRows; ++i) {
+    const uint32_t m = m0 + i;
+    if (m >= M) return;
+    const f32x4 lo = decode4<FMT>(code[i][0], scale_value(sb[i]));
+    const f32x4 hi = decode4<FMT>(code[i][kPer / 4 - 1], scale_value(sb[i]));
+    E* const to = static_cast<E*>(x) + (uint64_t)m * ldx + c;
+    u32x4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (DT == S2R_F32) v[w] = __float_as_uint(lo[w]);
+      else v[w] = w < 2 ? pack2<DT>(lo[2 * w], lo[2 * w + 1]) : pack2<DT>(hi[2 * w - 4], hi[2 * w - 3]);
+    }
+    if (c + kPer <= K) {
+      *reinterpret_cast<u32x4*>(to) = v;
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < kPer; ++e)
+        if (c + e < K) to[e] = DT == S2R_F32 ? (E)v[e % 4] : (E)(v[e / 2 % 4] >> 16 * (e % 2));
+    }
   }
 }
 
@@ -116,13 +138,13 @@ __global__ __launch_bounds__(kStoreThreads) void k_q8_weight(
     scale[(uint64_t)kb * lds + nb] = (uint8_t)sb;
     if (qt) scale_t[(uint64_t)nb * ldst + kb] = (uint8_t)sb;
   }
-  const float inv = scale_inverse(sb);
+  const float scale_f = scale_value(sb);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t rr = t / 8 + 32 * i, n = nb * kQ8Block + rr;
     float v[16];
     unpack16<DT>(r[i], v);
-    const u32x4 code = encode16<FMT>(v, inv);
+    const u32x4 code = encode16<FMT>(v, scale_f);
     if (n < N && c < K) store_codes16(q + (uint64_t)n * ldq, c, K, code);
     if (qt) {
 #pragma unroll
@@ -179,8 +201,8 @@ hipError_t launch_q8_save(uint64_t M, uint64_t K, const s2r_mat& x, const s2r_q8
 
 hipError_t launch_q8_load(uint64_t M, uint64_t K, const s2r_q8_mat& in, const s2r_mat& x,
                           hipStream_t s) {
-  const uint64_t ct = (K + kStoreBlocks * kQ8Block - 1) / (kStoreBlocks * kQ8Block);
-  const uint64_t rt = (M + kStoreRows - 1) / kStoreRows;
+  const uint64_t cols = 1024 / (x.dtype == S2R_F32 ? 4 : 2), rows = kStoreThreads / 64 * kLoadRows;
+  const uint64_t ct = (K + cols - 1) / cols, rt = (M + rows - 1) / rows;
   trace_mark(s, "k_q8_load");
   S2R_Q8_DISPATCH(x.dtype, in.format,
                   hipLaunchKernelGGL((k_q8_load<DT, FMT>), dim3((uint32_t)(ct * rt)),
