@@ -339,7 +339,7 @@ constexpr uint64_t kFewRows = 64;
 constexpr int kFewBatch = 2;  // blocks of the sum a wave has in flight
 
 __device__ inline i32x8 load_frag(const uint8_t* row, uint32_t k, uint32_t K) {
-  return join(load_codes16(row, k, K), load_codes16(row, k + 16, K));
+  return join(load_codes16(row, k, K), load_codes16(row, k + 64, K));
 }
 
 template <int FA, int FB, int FM, int WAVES>
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
     uint32_t sb[kFewBatch], sa[kFewBatch][FM];
 #pragma unroll
     for (int e = 0; e < kFewBatch; ++e) {
-      const uint32_t at = s + e * WAVES, k = at * kQ8Block + 32 * g;
+      const uint32_t at = s + e * WAVES, k = at * kQ8Block + 16 * g;  // and 64 further on: lines in whole halves
       if (at >= steps) continue;
       fb[e] = load_frag(row_b, k, K);
       sb[e] = scale_b[(uint64_t)at * b.lds];
@@ -453,15 +453,22 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
   if (M <= kFewRows) {
     trace_mark(s, "k_q8_gemm_few");
     const dim3 grid((n + 15) / 16);
-    if (M <= 16)
-      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 1, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
-    else if (M <= 32)
-      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 2, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
-    else
-      hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, 4, 8>), grid, dim3(512), 0, s, a, b, c, m, n, k);
+    // One workgroup for every compute unit or fewer: more waves each (4096 rows of B, one of A: 7.0
+    // us with 16, 8.3 with 8; 8192 rows: 11.9 and 10.7).
+    const bool sparse = grid.x <= kTileCus;
+#define S2R_FEW(FM, WAVES) \
+  hipLaunchKernelGGL((k_q8_gemm_few<FA, FB, FM, WAVES>), grid, dim3(64 * WAVES), 0, s, a, b, c, m, n, k)
+    if (M <= 16) {
+      if (sparse) S2R_FEW(1, 16);
+      else S2R_FEW(1, 8);
+    } else if (M <= 32) {
+      S2R_FEW(2, 8);
+    } else {
+      S2R_FEW(4, 8);
+    }
+#undef S2R_FEW
     return;
   }
-  trace_mark(s, "k_q8_gemm");
   GemmPlan p = gemm_plan(M, N, K);
   if (!workspace) p.cut = {1, p.blocks};
   const bool cut = p.cut.parts > 1;
