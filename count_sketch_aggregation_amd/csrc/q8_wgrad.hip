@@ -88,42 +88,59 @@ struct Feed {
   }
   // codes of the next block, with their scales (of a row beyond the end: any finite one, its codes
   // are 0; kWgradRows and kRows are multiples of 4, and so is `first`)
-  __device__ void fetch() {
+  __device__ void fetch(u32x4 (&c)[kLoads], uint32_t (&b)[kLoads]) {
     const auto v = view();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      next[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, at[j], 0, 0));
-      next_sb[j] = *reinterpret_cast<const uint32_t*>(scale + min(row + j * kRows, last) / 4 * 4);
+      c[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(v, at[j], 0, 0));
+      b[j] = *reinterpret_cast<const uint32_t*>(scale + min(row + j * kRows, last) / 4 * 4);
     }
     row += kWgradRows;
+    advance();
+  }
+  __device__ void fetch() { fetch(next, next_sb); }
+  __device__ void fetch_first() { fetch(code, sb); }
+  __device__ uint32_t own_scale(uint32_t b) const {  // of four rows; a lane's is the same in every block
+    return min(b >> row % 4 * 8 & 0xff, 254u) << 23;
+  }
+  // Half of the lanes decode and write their upper 16 bytes first: together the lanes of a write
+  // then meet every bank.
+  __device__ bool upper_first() const { return (threadIdx.x / 4 ^ threadIdx.x / 8) % 2; }
+  __device__ void put_code(int j, u32x4 c, uint32_t b) {
+    const bool swap = upper_first();
+    const uint32_t c0 = c[0], c1 = c[1], c2 = c[2], c3 = c[3];
+    code[j] = u32x4{swap ? c2 : c0, swap ? c3 : c1, swap ? c0 : c2, swap ? c1 : c3};
+    sb[j] = own_scale(b);
+  }
+  __device__ void settle_first() {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) put_code(j, code[j], sb[j]);
   }
   // The fetched codes become those that are decoded: moved here, where they are known to have
   // come, and not by the compiler further up.
   __device__ void take() {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
+      u32x4 c;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t c;
-        asm volatile("v_mov_b32 %0, %1" : "=v"(c) : "v"(next[j][w]));
-        code[j][w] = c;
+        uint32_t x;
+        asm volatile("v_mov_b32 %0, %1" : "=v"(x) : "v"(next[j][w]));
+        c[w] = x;
       }
-      uint32_t b;  // of four rows; this lane's is the same one in every block
+      uint32_t b;
       asm volatile("v_mov_b32 %0, %1" : "=v"(b) : "v"(next_sb[j]));
-      sb[j] = min(b >> row % 4 * 8 & 0xff, 254u) << 23;
+      put_code(j, c, b);
     }
   }
-  // Unit u decoded.  Half of the lanes write their upper 16 bytes first: together the lanes of
-  // a write then meet every bank.
+  // unit u decoded
   __device__ void decode(uint8_t* lds, int u) {
-    const bool swap = threadIdx.x / 8 % 2;
     const int j = u / 4, w = u % 4;
-    const u32x2 v = to_bf16<KIND == S2R_E5M2 ? S2R_E5M2 : S2R_E4M3>(
-        swap ? code[j][w ^ 2] : code[j][w], __uint_as_float(sb[j]));
+    const u32x2 v = to_bf16<KIND == S2R_E5M2 ? S2R_E5M2 : S2R_E4M3>(code[j][w], __uint_as_float(sb[j]));
     half[w % 2 * 2] = v[0];
     half[w % 2 * 2 + 1] = v[1];
     if (w % 2)
-      *reinterpret_cast<u32x4*>(lds + to + j * (kRows * kRowBytes) + ((w == 3) != swap ? 16 : 0)) = half;
+      *reinterpret_cast<u32x4*>(lds + to + j * (kRows * kRowBytes) + ((w == 3) != upper_first() ? 16 : 0)) = half;
   }
 };
 
@@ -191,11 +208,7 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgra
     };
     auto fetch = [&] {
       x.fetch();
-      x.advance();
-      if (!Y::kDirect) {
-        y.fetch();
-        y.advance();
-      }
+      if (!Y::kDirect) y.fetch();
     };
     auto take = [&] {
       x.take();
@@ -209,6 +222,8 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgra
         else if (!Y::kDirect) y.decode(lds + to, u - X::kUnits);
       }
     };
+    x.fetch_first();
+    if (!Y::kDirect) y.fetch_first();
     fetch();
     if (Y::kDirect) {
       load_y(here, 0, 1);
@@ -217,13 +232,13 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgra
       y.advance();
     }
     drain_and_sync();
-    take();
-    fetch();
+    x.settle_first();
+    if (!Y::kDirect) y.settle_first();
     decode(here, 0, kUnits);
-    drain_and_sync();
     take();
     fetch();
     decode(there, 0, kUnits / 4);
+    sync_reads();
     Frags f0, f1;
 #pragma unroll
     for (int e = 0; e < kReads; ++e) read(f0, lds + here, lds + here + Y::kBytes, 0, e);
