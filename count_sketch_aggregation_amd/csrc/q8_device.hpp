@@ -259,6 +259,16 @@ __device__ inline f32x4 decode4(uint32_t q, float scale) {
   return {lo[0], lo[1], hi[0], hi[1]};
 }
 
+// Four codes to bf16: exact, as a scale is a power of two and a stored value a normal bf16.
+template <int FMT>
+__device__ inline u32x2 to_bf16(uint32_t q, float scale) {
+  if (FMT == S2R_E4M3)
+    return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, true))};
+  return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, false)),
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, true))};
+}
+
 template <int FMT>
 __device__ inline void decode16(u32x4 q, float scale, float (&x)[16]) {
 #pragma unroll

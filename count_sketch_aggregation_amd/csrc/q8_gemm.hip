@@ -5,11 +5,22 @@
 // are consecutive columns of C.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
 namespace s2r {
+
+// f(first), ..., f(end - 1) with constants: the compiler gives up unrolling long bodies.
+template <int FIRST, class F, int... I>
+__device__ inline void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, FIRST + I>()), ...);
+}
+template <int FIRST, int END, class F>
+__device__ inline void each(F&& f) {
+  each_of<FIRST>(f, std::make_integer_sequence<int, END - FIRST>());
+}
 
 // ---- fragments ----------------------------------------------------------------------------
 // `at` is the byte of `sa` that holds this fragment's scale.
@@ -21,6 +32,13 @@ __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
     v[4 + i] = (int)hi[i];
   }
   return v;
+}
+
+// Codes 8 part .. + 7 of a lane's 32, as bf16.
+template <int FMT>
+__device__ inline bf16x8 widen8(const i32x8& c, int part, uint32_t sb) {
+  const u32x2 lo = to_bf16<FMT>(c[2 * part], scale_value(sb)), hi = to_bf16<FMT>(c[2 * part + 1], scale_value(sb));
+  return __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
 }
 
 __device__ inline void clear_from(i32x8& v, int left) {  // `left` bytes stay
@@ -57,6 +75,7 @@ __device__ inline f32x16 mma32(const i32x8& b, const i32x8& a, const f32x16& c, 
 // scales of a lane's fragments are one load.
 // A workgroup stays for several tiles, and the blocks of all of them are one stream: the next
 // tile's first blocks arrive while the last ones of this are multiplied and its results leave.
+__host__ __device__ constexpr int lesser(int a, int b) { return a < b ? a : b; }
 __device__ inline uint32_t spread(uint32_t p) { return p / 2 % 4 | p / 16 % 2 << 2; }
 
 // ROWS x 64 results from LDS: rows m0, m0 + step, ..., columns n0 .. n0 + 63; lane l takes eight
@@ -116,13 +135,14 @@ __device__ inline void store_turned(const s2r_mat& c, const uint8_t* lds, uint32
   }
 }
 
-template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL>
-__global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm(
+template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     s2r_q8_mat a, s2r_q8_mat b, s2r_mat c, uint64_t part_bytes, uint32_t M, uint32_t N, uint32_t K,
     uint32_t m_tiles, uint32_t n_tiles, uint32_t total, uint32_t part_blocks) {
   constexpr int kWaves = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
   constexpr int kLoadsA = TM / 8 / kWaves, kLoads = (TM + TN) / 8 / kWaves;
   constexpr int kBytes = (TM + TN) * kQ8Block;
+  static_assert(kLoads - kLoads * 5 / 8 <= FM * FN, "late loads have a slot each");
   constexpr int kTurnRows = kWaves > 4 ? 16 : 32, kTurn = kTurnRows * 64 * 4;  // a wave's results in LDS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBytes + kWaves * kTurn];
 
@@ -220,8 +240,20 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
 #pragma unroll
     for (int j = 0; j < FN; ++j) clear_from(f.b[j], left - 32 * (int)g);
   };
-  constexpr int kMma = FM * FN, kReads = 2 * (FM + FN);
-  constexpr int kRead = kMma * 5 / 16, kEarly = kLoads * 5 / 8;  // when reads end and loads begin
+  // A half is multiplied in kSlots instructions: one for each pair of fragments, or four where codes
+  // become bf16 (WIDE), eight of a lane's 32 at a time.  kRead of them cover the next half's
+  // reads, loads begin after that.
+  constexpr int kMma = FM * FN, kReads = 2 * (FM + FN), kSlots = WIDE ? 4 * kMma : kMma;
+  constexpr int kRead = kSlots * 5 / 16, kEarly = kLoads * 5 / 8;
+  struct Wide {
+    bf16x8 a[FM], b[FN];
+  };
+  Wide wide[2];
+  // fragment i of FN + FM, its eight codes number `part`
+  auto widen = [&](Wide& to, const Frags& f, int part, int i, uint32_t sa, uint32_t sb) {
+    if (i < FN) to.b[i] = widen8<FB>(f.b[i], part, sb);
+    else to.a[i - FN] = widen8<FA>(f.a[i - FN], part, sa >> 8 * (i - FN) & 0xff);
+  };
 
   uint8_t *here = lds, *there = lds + kBytes;
   uint32_t sa = 0, sb = 0, sa_ahead = 0, sb_ahead = 0;  // of this block and of the next
@@ -241,6 +273,8 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
     sync_but<kLoads>();
 #pragma unroll
     for (int e = 0; e < kReads; ++e) read(f0, here, 0, e);
+#pragma unroll
+    for (int i = 0; i < (WIDE ? FM + FN : 0); ++i) widen(wide[0], f0, 0, i, sa, sb);
   }
 
   for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
@@ -248,45 +282,75 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
     const uint32_t b0 = t.part * part_blocks, b1 = min(b0 + part_blocks, blocks);
     after = start_of(in.item + gridDim.x);
     f32x16 acc[FM][FN] = {};
-    auto multiply = [&](const Frags& f, int e) {
-      acc[e / FN][e % FN] = mma32<FA, FB>(f.b[e % FN], f.a[e / FN], acc[e / FN][e % FN], sb, sa, e / FN);
+    auto multiply = [&](const Frags& f, int slot) {
+      const int e = slot % kMma;
+      f32x16& to = acc[e / FN][e % FN];
+      if (WIDE) {
+        const Wide& w = wide[slot / kMma % 2];
+        to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w.b[e % FN], w.a[e / FN], to, 0, 0, 0);
+      } else {
+        to = mma32<FA, FB>(f.b[e % FN], f.a[e / FN], to, sb, sa, e / FN);
+      }
+    };
+    // beside the products of one part: the next part's codes, or the next half's first ones
+    auto widen_ahead = [&](const Frags& f, const Frags& next, int slot, uint32_t sa_next, uint32_t sb_next) {
+      if (!WIDE) return;
+      const int part = slot / kMma, e = slot % kMma;
+#pragma unroll
+      for (int i = e * (FM + FN) / kMma; i < (e + 1) * (FM + FN) / kMma; ++i) {
+        if (part < 3) widen(wide[(part + 1) % 2], f, part + 1, i, sa, sb);
+        else widen(wide[0], next, 0, i, sa_next, sb_next);
+      }
     };
     auto run = [&](auto clear, uint32_t block) {  // one block, without the codes at or beyond K
-      if (clear) clear_tail(f0, (int)(K - block * kQ8Block));
+      if (clear) {
+        clear_tail(f0, (int)(K - block * kQ8Block));
 #pragma unroll
-      for (int e = 0; e < kRead; ++e) {
+        for (int i = 0; i < (WIDE ? FM + FN : 0); ++i) widen(wide[0], f0, 0, i, sa, sb);
+      }
+      each<0, kRead>([&](auto e) {
         multiply(f0, e);
 #pragma unroll
         for (int q = e * kReads / kRead; q < (e + 1) * kReads / kRead; ++q) read(f1, here, 1, q);
         if (e == 0) advance();
+        widen_ahead(f0, f1, e, sa, sb);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
       multiply(f0, kRead);
+      widen_ahead(f0, f1, kRead, sa, sb);
       sync_reads();  // this block's LDS is free
       const Views v = views();
-#pragma unroll
-      for (int e = kRead + 1; e < kMma; ++e) {
+      each<kRead + 1, kSlots>([&](auto e) {
+        constexpr int kAt = e - kRead - 1, kOf = kSlots - kRead - 1;
         multiply(f0, e);
 #pragma unroll
-        for (int q = (e - kRead - 1) * kEarly / (kMma - kRead - 1); q < (e - kRead) * kEarly / (kMma - kRead - 1); ++q)
-          load(here, v, q);
+        for (int q = kAt * kEarly / kOf; q < (kAt + 1) * kEarly / kOf; ++q) load(here, v, q);
+        if (!(clear && e / kMma == 3)) widen_ahead(f0, f1, e, sa, sb);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
       sync_but<kEarly>();  // the next block is there
       // moved here, where their loads are known to be done, and not by the compiler further up
       uint32_t sa_next, sb_next;
       asm volatile("v_mov_b32 %0, %1" : "=v"(sa_next) : "v"(sa_ahead));
       asm volatile("v_mov_b32 %0, %1" : "=v"(sb_next) : "v"(sb_ahead));
       load_scales(sa_ahead, sb_ahead);
-      if (clear) clear_tail(f1, (int)(K - block * kQ8Block) - 64);
+      if (clear) {
+        clear_tail(f1, (int)(K - block * kQ8Block) - 64);
 #pragma unroll
-      for (int e = 0; e < kMma; ++e) {
+        for (int i = 0; i < (WIDE ? FM + FN : 0); ++i) widen(wide[0], f1, 0, i, sa, sb);
+      }
+      constexpr int kReadLate = WIDE ? 3 * kMma : kMma;  // its first codes are widened after that
+      each<0, kSlots>([&](auto e) {
         multiply(f1, e);
 #pragma unroll
-        for (int q = e * kReads / kMma; q < (e + 1) * kReads / kMma; ++q) read(f0, there, 0, q);
-        if (kEarly + e < kLoads) load(here, v, kEarly + e);
+        for (int q = e * kReads / kReadLate; q < lesser((e + 1) * kReads / kReadLate, kReads); ++q)
+          read(f0, there, 0, q);
+#pragma unroll
+        for (int q = kEarly + e * kMma / kSlots; q < lesser(kEarly + (e + 1) * kMma / kSlots, kLoads); ++q)
+          load(here, v, q);
+        widen_ahead(f1, f0, e, sa_next, sb_next);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
       uint8_t* const x = here;
       here = there;
       there = x;
@@ -326,11 +390,6 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_gemm
 }
 
 // ---- few rows: fragments of 16 rows --------------------------------------------------------
-template <int FA, int FB>
-__device__ inline f32x4 mma(const i32x8& b, const i32x8& a, const f32x4& c, uint32_t sb, uint32_t sa) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, FB, FA, 0, (int)sb, 0, (int)sa);
-}
-
 // ---- few rows -----------------------------------------------------------------------------
 // Up to 16 FM rows of A: the rows of B are read once, straight into registers, and bound the
 // call.  A workgroup takes 16 of them and cuts the sum among its waves, block by block in
@@ -378,8 +437,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
     for (int e = 0; e < kFewBatch; ++e) {
       if (s + e * WAVES >= steps) continue;
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        acc[i] = mma<FA, FB>(fb[e], fa[e][i], acc[i], sb[e], sa[e][i]);
+      for (int p = 0; p < 4; ++p) {
+        const bf16x8 wb = widen8<FB>(fb[e], p, sb[e]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, widen8<FA>(fa[e][i], p, sa[e][i]), acc[i], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
@@ -421,9 +484,9 @@ struct GemmPlan {
   uint32_t tm, tn, mt, nt, blocks;
   Cut cut;
 };
-GemmPlan gemm_plan(uint64_t M, uint64_t N, uint64_t K) {
-  static constexpr uint32_t kTiles[][4] = {
-      {256, 256, 1350, 8000}, {256, 128, 900, 6000}, {128, 128, 680, 5000}};
+GemmPlan gemm_plan(uint64_t M, uint64_t N, uint64_t K, bool wide) {
+  static constexpr uint32_t kTiles[][5] = {
+      {256, 256, 1350, 2700, 8000}, {256, 128, 900, 1500, 6000}, {128, 128, 680, 900, 5000}};
   const uint32_t blocks = (uint32_t)((K + kQ8Block - 1) / kQ8Block);
   GemmPlan best = {};
   uint64_t least = ~0ull;
@@ -437,7 +500,7 @@ GemmPlan gemm_plan(uint64_t M, uint64_t N, uint64_t K) {
                         tiles * parts > kTileCus))
         continue;  // as few parts give the same, or one has a single block beside longer ones
       const uint64_t rounds = (tiles * parts + kTileCus - 1) / kTileCus;
-      uint64_t ns = rounds * ((uint64_t)p.cut.blocks * t[2] + t[3]);
+      uint64_t ns = rounds * ((uint64_t)p.cut.blocks * t[wide ? 3 : 2] + t[4]);
       if (parts > 1) ns += 3000 + M * N * 4 * (2 * parts + 1) / 4000;
       if (ns < least) least = ns, best = p;
     }
@@ -475,7 +538,8 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
 #undef S2R_FEW
     return;
   }
-  GemmPlan p = gemm_plan(M, N, K);
+  const bool wide = c.dtype == S2R_F32;
+  GemmPlan p = gemm_plan(M, N, K, wide);
   if (!workspace) p.cut = {1, p.blocks};
   const bool cut = p.cut.parts > 1;
   s2r_mat out = c;
@@ -483,20 +547,26 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
   const uint64_t part_bytes = M * out.ld * sizeof(float);
   const uint32_t total = p.mt * p.nt * p.cut.parts;
   const dim3 grid(std::min(total, kTileCus));
-#define S2R_TILE(FM, FN, TAIL)                                                                    \
-  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, FM, FN, TAIL>), grid, dim3(256), 0, s, a, b, out,    \
-                     part_bytes, m, n, k, p.mt, p.nt, total, p.cut.blocks)
+#define S2R_TILE(FM, FN, TAIL, WIDE)                                                               \
+  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, FM, FN, TAIL, WIDE>), grid, dim3(256), 0, s, a, b,    \
+                     out, part_bytes, m, n, k, p.mt, p.nt, total, p.cut.blocks)
+#define S2R_TILE_TAIL(FM, FN, WIDE)                          \
+  do {                                                       \
+    if (k % kQ8Block == 0) S2R_TILE(FM, FN, false, WIDE);    \
+    else S2R_TILE(FM, FN, true, WIDE);                       \
+  } while (0)
   trace_mark(s, "k_q8_gemm");
-  if (p.tm == 256 && p.tn == 256) {
-    if (k % kQ8Block == 0) S2R_TILE(4, 4, false);
-    else S2R_TILE(4, 4, true);
+  if (p.tn == 256) {
+    if (wide) S2R_TILE_TAIL(4, 4, true);
+    else S2R_TILE_TAIL(4, 4, false);
   } else if (p.tm == 256) {
-    if (k % kQ8Block == 0) S2R_TILE(4, 2, false);
-    else S2R_TILE(4, 2, true);
+    if (wide) S2R_TILE_TAIL(4, 2, true);
+    else S2R_TILE_TAIL(4, 2, false);
   } else {
-    if (k % kQ8Block == 0) S2R_TILE(2, 2, false);
-    else S2R_TILE(2, 2, true);
+    if (wide) S2R_TILE_TAIL(2, 2, true);
+    else S2R_TILE_TAIL(2, 2, false);
   }
+#undef S2R_TILE_TAIL
 #undef S2R_TILE
   if (!cut) return;
   trace_mark(s, "k_q8_gemm_sum");
@@ -510,8 +580,9 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
 
 size_t q8_gemm_workspace(uint64_t M, uint64_t N, uint64_t K) {
   if (few_rows(M, N, K, true)) return 0;
-  const GemmPlan p = gemm_plan(M, N, K);
-  return p.cut.parts > 1 ? p.cut.parts * M * ((N + 3) / 4 * 4) * sizeof(float) : 0;
+  // for either kind of result
+  const uint32_t parts = std::max(gemm_plan(M, N, K, false).cut.parts, gemm_plan(M, N, K, true).cut.parts);
+  return parts > 1 ? parts * M * ((N + 3) / 4 * 4) * sizeof(float) : 0;
 }
 
 hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a,

@@ -13,16 +13,6 @@ namespace s2r {
 constexpr int kWgradRows = 64;  // rows m of a block of the sum
 constexpr int kBf16 = 2;        // kind of an operand that is bf16 already (else its q8 format)
 
-// Four codes to bf16: exact, as a scale is a power of two and a stored value a normal bf16.
-template <int FMT>
-__device__ inline u32x2 to_bf16(uint32_t q, float scale) {
-  if (FMT == S2R_E4M3)
-    return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, false)),
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, true))};
-  return {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, false)),
-          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q, scale, true))};
-}
-
 // An operand on its way to LDS, a block of 64 rows x COLS columns at a time, bf16 there: 64-byte
 // piece s of row p lies at s ^ (p % 4).  What is bf16 already goes there directly; codes come
 // to registers first and are decoded from there.  Rows at or beyond the end give zeros.

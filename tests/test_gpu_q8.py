@@ -214,6 +214,28 @@ def test_gemm_on_ordinary_values(M, N, K, fa, fb):
             assert bool(((got - want).abs() <= tol).all()), (out, with_ws)
 
 
+@pytest.mark.parametrize("M", [1, 20, 60, 130, 300])
+@pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
+def test_gemm_in_fp32_keeps_small_products_beside_large_ones(M, fa):
+    """2^16 and 2^-6 among the products of one block of the sum: fp32 holds all of it."""
+    gp.say(f"gemm small beside large M={M} {fa}")
+    N, K = 140, 400
+    g = _gen(12)
+    va, vb = torch.zeros((M, K), dtype=torch.float64), torch.zeros((N, K), dtype=torch.float64)
+    big = torch.randint(0, K // 2, (1,), generator=g).item() * 2
+    va[:, big], vb[:, big] = 2.0 ** 8, 2.0 ** 8
+    for at in (big + 1, (big + 7) % K, (big + 40) % K, (big + 190) % K):
+        va[:, at] = 2.0 ** -3 * torch.randint(0, 2, (M,), generator=g)
+        vb[:, at] = 2.0 ** -3 * torch.randint(-1, 2, (N,), generator=g)
+    code = lambda v, f: v.float().to(ref.F8[f]).view(torch.uint8)
+    a = stored(code(va, fa), torch.full((M, 4), 127), fa)
+    b = stored(code(vb, "e4m3"), torch.full((2, 4), 127), "e4m3", True)
+    want = va @ vb.t()
+    assert len(want.unique()) > 1
+    for with_ws in (False, True):
+        assert torch.equal(gemm(M, N, K, a, b, "f32", with_ws).double(), want)
+
+
 def test_gemm_takes_wide_scales():
     """Scales over the whole range a stored matrix can have, in one row and in one column."""
     gp.say("gemm wide scales")
