@@ -1,8 +1,20 @@
 // q8_gemm.hip -- C = A B^T of 8-bit matrices with a power-of-two scale for each block of 128:
 //   c[m][n] = sum_k a[m][k] sa[k / 128][m] b[n][k] sb[k / 128][n / 128].
-// The scaled matrix instruction multiplies both operands by their scales itself, so one fp32
-// accumulator runs over the whole sum.  The first operand is B, so that a lane's results
-// are consecutive columns of C.
+// The first operand of every matrix instruction is B, so that a lane's results are consecutive
+// columns of C; one fp32 accumulator runs over the whole sum.
+//
+// Two ways through the matrix cores.  The scaled 8-bit instruction multiplies both operands by
+// their scales itself and runs at twice the rate of bf16, but it adds the products of
+// neighbouring k with only about 13 bits below the largest (2^16 + 2^2 gives 2^16; products further
+// apart and the accumulator keep 24).  Results in 16 bits hide that: they are off by 2.1e-4 (fp16) and
+// 1.6e-3 (bf16) of their size either way.  An fp32 result would be off by 2.4e-5 instead of 7e-8,
+// so fp32 results and the few-row form, which memory bounds, decode to bf16, exact for every stored
+// value, and use the bf16 instruction.
+//
+// Measured on MI355X: 16384 x 8192 x 4096 e4m3 to bf16 422 us, 2.6 PFLOP/s (a library's product with one
+// scale for a whole matrix 381); with K = 8192 2.9.  A block of the sum of a 256 x 256 tile takes
+// 2400 to 2700 cycles where its matrix instructions alone take 2048; zeros run 18% faster than
+// random codes, so the rest is mostly power.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

@@ -3,6 +3,11 @@
 // The checkpoint's scale changes along m, the summed index, so the scaled matrix instruction
 // cannot apply it: both operands become bf16, which holds every stored value exactly, and
 // the products are summed in fp32 by the bf16 matrix instruction.
+//
+// Measured on MI355X: 16384 x 4096 x 4096 from bf16 gradients 459 us, 1.2 PFLOP/s, as a library's
+// bf16 product of the same layout (454; 339 where the sum's index is the contiguous one).  Its LDS is
+// busy for half of the cycles (read 768, written 512 of about 3400 a block) and zeros run 20%
+// faster than random values.
 #include <algorithm>
 
 #include "q8_launch.hpp"

@@ -50,3 +50,23 @@ def test_training_learns(example):
     losses = example.train(steps=30, log=None)
     assert all(l == l for l in losses)
     assert losses[-1] < 0.5 * losses[0]
+
+
+def test_readme_examples():
+    """Every Python example of README.md, one after the other; the 8-bit layer against its inputs.
+    A value is off by at most 2^-4 of itself after storage: y by the sum of |x w| times
+    2 * 2^-4 + 2^-8 and its rounding, dw (dy is ones) by the sum of |x| times 2^-4; each doubled for
+    values below their format's normal range."""
+    import re
+    gp.say("readme examples")
+    src = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    env: dict = {}
+    for code in re.findall(r"```python\n(.*?)```", src, re.S):
+        exec(compile(code, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    x, w = env["x"].double().cpu(), env["w"].double().cpu()
+    y, dw = env["y"].double().cpu(), env["grads"][0, :w.numel()].view(w.shape).double().cpu()
+    mass = x.abs() @ w.abs().t()
+    assert bool(((y - x @ w.t()).abs() <= 2 * (2 * 2.0 ** -4 + 2.0 ** -8) * mass).all())
+    want = x.sum(0).expand_as(w)
+    assert bool(((dw - want).abs() <= 2 * 2.0 ** -4 * x.abs().sum(0)).all())
