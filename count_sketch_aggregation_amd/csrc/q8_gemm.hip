@@ -201,7 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     x.lane_scale = min(m0 + wm + FM * r, (uint32_t)a.lds - FM);
     return x;
   };
-  At in, after;
+  At in = {}, after = {};
   auto advance = [&] {  // without a branch: it runs between matrix instructions
     in.left = __builtin_amdgcn_readfirstlane(in.left);
     const bool go = in.left == 0, on = in.left + 1 > 1;

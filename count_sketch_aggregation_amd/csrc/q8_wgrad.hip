@@ -329,30 +329,37 @@ __global__ __launch_bounds__(kSumThreads) void k_q8_wgrad_sum(const float* __res
 
 namespace {
 
-// Tiles of 256 x 256 where each compute unit gets kWgradDeep blocks of 64 rows or more of them,
-// as it holds one such workgroup; tiles of 128 x 128 otherwise, two of which fit one.  Measured: 8192 x
-// 2048 x 2048 (32 blocks) 88 us in tiles of 256, 95 in tiles of 128; 4096 x 2048 x 2048 (16) 60 and 56.
-constexpr uint64_t kWgradDeep = 24;
-constexpr uint64_t kWgradLeast = 4;  // blocks of a part
-
+// Tiles and parts of the sum with the least estimated time, in nanoseconds.  A tile of 256 x 256
+// takes 1600 for a block of 64 rows and 9000 to begin and to leave, one of 128 x 128 1100 and 6000
+// (loads' latency: two of them on a compute unit take hardly longer than one).  Parts are written and read
+// again, at 5 bytes a picosecond, by a launch of 2000.  Measured: 8192 x 2048 x 2048 88 us in tiles
+// of 256 and 4 parts, 95 in tiles of 128 and 2; 4096 x 2048 x 2048 60 and 56; 700 x 2000 x 2000 28 in
+// 2 parts, 19 in one.
 struct WgradPlan {
   uint32_t side, nt, kt;  // of the tiles
   Cut cut;
   uint64_t part_floats;
 };
 WgradPlan wgrad_plan(uint64_t M, uint64_t N, uint64_t K) {
-  WgradPlan p;
-  auto tiles = [&](uint64_t side) { return ((N + side - 1) / side) * ((K + side - 1) / side); };
-  const uint64_t blocks = (M + kWgradRows - 1) / kWgradRows;
-  p.side = tiles(256) * blocks >= kWgradDeep * kTileCus ? 256 : 128;
-  p.nt = (uint32_t)((N + p.side - 1) / p.side);
-  p.kt = (uint32_t)((K + p.side - 1) / p.side);
-  // one 256-side workgroup fits a compute unit, two of the others
-  const uint64_t room = p.side == 256 ? kTileCus : 2 * kTileCus;
-  const uint64_t parts = std::min(room / std::max<uint64_t>(1, tiles(p.side)), blocks / kWgradLeast);
-  p.cut = cut_evenly((uint32_t)blocks, (uint32_t)std::max<uint64_t>(1, parts));
-  p.part_floats = N * ((K + 3) / 4 * 4);
-  return p;
+  static constexpr uint32_t kTiles[][4] = {{256, kTileCus, 1600, 9000}, {128, 2 * kTileCus, 1100, 6000}};
+  const uint32_t blocks = (uint32_t)((M + kWgradRows - 1) / kWgradRows);
+  const uint64_t part_floats = N * ((K + 3) / 4 * 4);
+  WgradPlan best = {};
+  uint64_t least = ~0ull;
+  for (const auto& t : kTiles) {
+    WgradPlan p = {t[0], (uint32_t)((N + t[0] - 1) / t[0]), (uint32_t)((K + t[0] - 1) / t[0]), {1, blocks},
+                   part_floats};
+    const uint64_t tiles = (uint64_t)p.nt * p.kt;
+    for (uint32_t parts = 1; parts <= 64; ++parts) {
+      p.cut = cut_evenly(blocks, parts);
+      if (parts > 1 && (p.cut.parts != parts || tiles * parts > t[1])) continue;
+      const uint64_t rounds = (tiles * parts + t[1] - 1) / t[1];
+      uint64_t ns = rounds * ((uint64_t)p.cut.blocks * t[2] + t[3]);
+      if (parts > 1) ns += 2000 + part_floats * 4 * (2 * parts + 1) / 5000;
+      if (ns < least) least = ns, best = p;
+    }
+  }
+  return best;
 }
 
 template <int KY, int FX>
