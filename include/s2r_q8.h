@@ -98,7 +98,7 @@ size_t s2r_q8_gemm_workspace_bytes(uint64_t M, uint64_t N, uint64_t K);
 /* c[m][n] = sum over k < K of value(a[m][k]) * value(b[n][k]).
  * a [M][K] row blocks, b [N][K] square blocks, c [M][N] of any s2r_dtype, rounded once from a
  * sum in fp32.  For a c in fp32 every product is exact and every addition fp32.  For a c in 16
- * bits and M > 64 the products go through the 8-bit matrix instruction, which adds neighbouring
+ * bits and M > 32 the products may go through the 8-bit matrix instruction, which adds neighbouring
  * products of a row with about 13 bits below the largest of them: 2.4e-5 of a result's typical
  * size (root mean square, 5001 x 1000 x 4100), where rounding to fp16 costs 2e-4 and to bf16 1.6e-3.
  * Layer output: a = X, b = W [N][K].  Input gradient: a = dY, b = the

@@ -390,6 +390,27 @@ def test_wgrad_scales_along_the_sum():
     assert torch.equal(got, sel.t() @ vx)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e5m2"])
+def test_scale_padding_may_hold_anything(kind):
+    """The scale bytes behind a matrix's last row are not a number; M is not a multiple of 4."""
+    gp.say(f"scale padding {kind}")
+    M, N, K = 131, 150, 260
+    x, vx = integers(M, K, "e4m3", 8)
+    x.scales[:, M:] = 0xFF
+    if kind == "bf16":
+        vy = torch.randint(-3, 4, (M, N), generator=_gen(7)).double()
+        dy = s2r.mat(wide(M, N, "bf16", x=vy)[:, :N])
+    else:
+        dy, vy = integers(M, N, kind, 7)
+        dy.scales[:, M:] = 0xFF
+    for with_ws in (False, True):
+        assert torch.equal(wgrad(M, N, K, dy, x, with_ws=with_ws), vy.t() @ vx)
+    b, vb = integers(N, K, "e4m3", 2, True)
+    b.scales[:, 2:] = 0xFF
+    for out in ("f32", "bf16"):
+        assert torch.equal(gemm(M, N, K, x, b, out, True), (vx @ vb.t()).to(ref.DTYPES[out]))
+
+
 def test_wgrad_keeps_non_finite_values_in_their_row():
     gp.say("wgrad non-finite")
     M, N, K = 100, 140, 150
