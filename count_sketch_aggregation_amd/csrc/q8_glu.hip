@@ -10,8 +10,10 @@
 //              (1 + tanh z) / 2:              act = g s,  act' = s + g s (1 - s) 2 z'
 // Element-wise apart from the blocks' largest magnitudes: one read and one write of
 // everything, bound by HBM.  Measured on MI355X: gated SiLU of 8192 x 8192 bf16 with its three 8-bit
-// results 87 us (5.4 TB/s), its gradient 80 us (5.0); with the library's exponential and division the
-// gradient took 97 and was bound by arithmetic.
+// results 87 us (5.4 TB/s), its gradient 83 us (4.9); with the library's exponential and division the
+// gradient took 97 and was bound by arithmetic.  GELU takes 95 and 113; by the complementary error
+// function, exact far below zero where 1 + erf loses all digits, it took 123 and 146 for values
+// that a block's scale rounds away.
 #include "q8_device.hpp"
 #include "q8_launch.hpp"
 
@@ -21,10 +23,23 @@ constexpr int kGluThreads = 256;
 constexpr int kGluRows = kGluThreads / 8;
 constexpr int kGluBlocks = 2;  // blocks of 128 columns per workgroup: two or three streams each
 
-// The hardware's 2^x and reciprocal, each within a unit in the last place: what follows is
-// rounded to 8 or 16 bits.
+// e^x within two units in the last place at every x: x log2(e) is cut into a whole number and a
+// rest that keeps its low bits, and the hardware's 2^x (one unit) takes the rest.  Without that the
+// argument's rounding alone costs |x| half units, and a result next to a border of the 8-bit
+// grid falls to the other side that much more often.  Beyond +-200 it is infinite or zero; a NaN gets
+// lost, but what exp_of's callers multiply it with is the same NaN.
+__device__ inline float exp_of(float x) {
+  x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
+  const float n = __builtin_rintf(x * 1.44269504088896f);
+  float r = __builtin_fmaf(x, 1.44269504088896f, -n);
+  r = __builtin_fmaf(x, 1.925963033500e-8f, r);  // log2(e) beyond 24 bits
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(r), (int)n);
+}
+
+// The hardware's reciprocal with one step of Newton's.
 __device__ inline float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+  const float d = 1.0f + exp_of(-x), r = __builtin_amdgcn_rcpf(d);
+  return d < __builtin_inff() ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r;
 }
 
 template <int ACT>
@@ -44,7 +59,7 @@ __device__ inline void act_both(float g, float& a, float& d) {
   } else if (ACT == S2R_ACT_GELU) {
     const float c = 0.5f + 0.5f * erff(g * 0.70710678118654752f);
     a = g * c;
-    d = c + g * (__builtin_amdgcn_exp2f(-0.72134752044448170f * g * g) * 0.39894228040143268f);
+    d = c + g * (exp_of(-0.5f * g * g) * 0.39894228040143268f);
   } else {
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float s = sigmoid(z2);
