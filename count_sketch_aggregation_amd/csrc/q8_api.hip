@@ -55,6 +55,22 @@ s2r_status done(hipError_t e, void* stream) {
   return S2R_OK;
 }
 
+s2r_status gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat* a, const s2r_q8_mat* b,
+                const s2r_mat* c, bool fast, void* workspace, size_t ws_bytes, void* stream) {
+  if (!a || !b || !c) return S2R_ERR_NULL;
+  Verdict v;
+  if (!sizes_ok(M, N, K)) v.add(S2R_ERR_DIM);
+  v.add(check(a, M, K, M));
+  v.add(check(b, N, K, blocks128(N)));
+  v.add(check(c, M, N));
+  if (v.st != S2R_OK) return v.st;
+  if (M == 0 || N == 0) return S2R_OK;
+  v.add(check_workspace(workspace, ws_bytes, q8_gemm_workspace(M, N, K)));
+  if (v.st != S2R_OK) return v.st;
+  return done(launch_q8_gemm(M, N, K, *a, *b, *c, fast, ws_bytes ? workspace : nullptr, on(stream)),
+              stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -106,18 +122,13 @@ size_t s2r_q8_gemm_workspace_bytes(uint64_t M, uint64_t N, uint64_t K) {
 s2r_status s2r_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat* a,
                        const s2r_q8_mat* b, const s2r_mat* c, void* workspace, size_t ws_bytes,
                        void* stream) {
-  if (!a || !b || !c) return S2R_ERR_NULL;
-  Verdict v;
-  if (!sizes_ok(M, N, K)) v.add(S2R_ERR_DIM);
-  v.add(check(a, M, K, M));
-  v.add(check(b, N, K, blocks128(N)));
-  v.add(check(c, M, N));
-  if (v.st != S2R_OK) return v.st;
-  if (M == 0 || N == 0) return S2R_OK;
-  v.add(check_workspace(workspace, ws_bytes, q8_gemm_workspace(M, N, K)));
-  if (v.st != S2R_OK) return v.st;
-  return done(launch_q8_gemm(M, N, K, *a, *b, *c, ws_bytes ? workspace : nullptr, on(stream)),
-              stream);
+  return gemm(M, N, K, a, b, c, false, workspace, ws_bytes, stream);
+}
+
+s2r_status s2r_q8_gemm_fast(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat* a,
+                            const s2r_q8_mat* b, const s2r_mat* c, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  return gemm(M, N, K, a, b, c, true, workspace, ws_bytes, stream);
 }
 
 size_t s2r_q8_wgrad_workspace_bytes(uint64_t M, uint64_t N, uint64_t K) {

@@ -3,18 +3,22 @@
 // The first operand of every matrix instruction is B, so that a lane's results are consecutive
 // columns of C; one fp32 accumulator runs over the whole sum.
 //
-// Two ways through the matrix cores.  The scaled 8-bit instruction multiplies both operands by
-// their scales itself and runs at twice the rate of bf16, but it adds the products of
-// neighbouring k with only about 13 bits below the largest (2^16 + 2^2 gives 2^16; products further
-// apart and the accumulator keep 24).  Results in 16 bits hide that: they are off by 2.1e-4 (fp16) and
-// 1.6e-3 (bf16) of their size either way.  An fp32 result would be off by 2.4e-5 instead of 7e-8,
-// so fp32 results and the few-row form, which memory bounds, decode to bf16, exact for every stored
-// value, and use the bf16 instruction.
+// Two ways through the matrix cores.  s2r_q8_gemm and the few-row form, which memory bounds, decode to
+// bf16, exact for every stored value, and use the bf16 instruction, whose sums are fp32.
+// s2r_q8_gemm_fast gives the codes to the scaled 8-bit instruction, which multiplies both
+// operands by their scales itself and runs at twice the rate, but cuts products: of eight
+// neighbouring k (aligned to eight) each is cut toward zero at 2^-13 of the largest one's power of two
+// before they are added (2^16 - 2^16 + 2^3 gives 2^3, 2^16 - 2^16 + 2^2 gives 0; a subnormal code
+// counts as the format's least normal); these sums and the accumulator are added as fp32.  Where
+// nothing cancels a 16-bit result hides that (root mean square 2.4e-5 of its size, rounding costs
+// 2e-4 in fp16), but a sum that cancels does not, whatever type it is rounded to: so the caller
+// chooses.
 //
-// Measured on MI355X: 16384 x 8192 x 4096 e4m3 to bf16 422 us, 2.6 PFLOP/s (a library's product with one
-// scale for a whole matrix 381); with K = 8192 2.9.  A block of the sum of a 256 x 256 tile takes
-// 2400 to 2700 cycles where its matrix instructions alone take 2048; zeros run 18% faster than
-// random codes, so the rest is mostly power.
+// Measured on MI355X, 16384 x 8192 x 4096 e4m3 to bf16, many passes in turn over three sets of inputs:
+// s2r_q8_gemm 757 us, 1.45 PFLOP/s (a library's product of bf16 matrices 720), s2r_q8_gemm_fast 427 us,
+// 2.57 PFLOP/s (a library's with one scale for a whole matrix 391).  There a block of the sum of a
+// 256 x 256 tile takes 2400 to 2700 cycles where its matrix instructions alone take 2048; zeros run
+// 18% faster than random codes, so the rest is mostly power.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -488,9 +492,9 @@ __global__ __launch_bounds__(kSumThreads) void k_q8_gemm_sum(const float* __rest
 namespace {
 
 // Tiles and parts of the sum with the least estimated time, in nanoseconds.  A tile of 256 x 256
-// takes 1350 for a block of the sum and 8000 to begin and to leave, one of 256 x 128 900 and
-// 6000, one of 128 x 128 680 and 5000 (measured at K = 4096 with one tile on every compute
-// unit), and the compute units take them in rounds.  Parts are written and read again, at 4
+// takes 1350 for a block of the sum (2700 by way of bf16) and 8000 to begin and to leave, one of
+// 256 x 128 900 (1500) and 6000, one of 128 x 128 680 (900) and 5000 (measured at K = 4096 with one
+// tile on every compute unit), and the compute units take them in rounds.  Parts are written and read again, at 4
 // bytes a picosecond, by a launch of 3000.
 struct GemmPlan {
   uint32_t tm, tn, mt, nt, blocks;
@@ -529,7 +533,7 @@ bool few_rows(uint64_t M, uint64_t N, uint64_t K, bool workspace) {
 
 template <int FA, int FB>
 void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_q8_mat& b,
-             const s2r_mat& c, void* workspace, hipStream_t s) {
+             const s2r_mat& c, bool fast, void* workspace, hipStream_t s) {
   const uint32_t m = (uint32_t)M, n = (uint32_t)N, k = (uint32_t)K;
   if (few_rows(M, N, K, workspace != nullptr)) {
     trace_mark(s, "k_q8_gemm_few");
@@ -550,7 +554,7 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
 #undef S2R_FEW
     return;
   }
-  const bool wide = c.dtype == S2R_F32;
+  const bool wide = !fast;
   GemmPlan p = gemm_plan(M, N, K, wide);
   if (!workspace) p.cut = {1, p.blocks};
   const bool cut = p.cut.parts > 1;
@@ -592,20 +596,20 @@ void go_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a, const s2r_
 
 size_t q8_gemm_workspace(uint64_t M, uint64_t N, uint64_t K) {
   if (few_rows(M, N, K, true)) return 0;
-  // for either kind of result
+  // for s2r_q8_gemm and s2r_q8_gemm_fast
   const uint32_t parts = std::max(gemm_plan(M, N, K, false).cut.parts, gemm_plan(M, N, K, true).cut.parts);
   return parts > 1 ? parts * M * ((N + 3) / 4 * 4) * sizeof(float) : 0;
 }
 
 hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a,
-                          const s2r_q8_mat& b, const s2r_mat& c, void* workspace,
+                          const s2r_q8_mat& b, const s2r_mat& c, bool fast, void* workspace,
                           hipStream_t s) {
   if (a.format == S2R_E4M3) {
-    if (b.format == S2R_E4M3) go_gemm<S2R_E4M3, S2R_E4M3>(M, N, K, a, b, c, workspace, s);
-    else go_gemm<S2R_E4M3, S2R_E5M2>(M, N, K, a, b, c, workspace, s);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E4M3, S2R_E4M3>(M, N, K, a, b, c, fast, workspace, s);
+    else go_gemm<S2R_E4M3, S2R_E5M2>(M, N, K, a, b, c, fast, workspace, s);
   } else {
-    if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, workspace, s);
-    else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, workspace, s);
+    if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, fast, workspace, s);
+    else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, fast, workspace, s);
   }
   return hipGetLastError();
 }

@@ -15,7 +15,8 @@ hipError_t launch_q8_weight(uint64_t N, uint64_t K, const s2r_mat& w, const s2r_
 
 size_t q8_gemm_workspace(uint64_t M, uint64_t N, uint64_t K);
 hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& a,
-                          const s2r_q8_mat& b, const s2r_mat& c, void* workspace, hipStream_t s);
+                          const s2r_q8_mat& b, const s2r_mat& c, bool fast, void* workspace,
+                          hipStream_t s);
 
 size_t q8_wgrad_workspace(uint64_t M, uint64_t N, uint64_t K);
 hipError_t launch_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy16,

@@ -8,6 +8,7 @@
  *   s2r_q8_load      8 bits -> bf16 / fp16 / fp32
  *   s2r_q8_weight    weights -> 8 bits, a scale per 128 x 128 block, and the transposed copy
  *   s2r_q8_gemm      C = A B^T of 8-bit matrices: layer output and input gradient
+ *   s2r_q8_gemm_fast the same at the 8-bit matrix rate, with products cut short
  *   s2r_q8_wgrad     dW (+)= dY^T X from the checkpoint of X: weight gradient
  *   s2r_q8_glu       y = act(g) * u with checkpoints of g and u
  *   s2r_q8_glu_grad  its gradient from those checkpoints
@@ -91,16 +92,13 @@ s2r_status s2r_q8_load(uint64_t M, uint64_t K, const s2r_q8_mat* in, const s2r_m
 s2r_status s2r_q8_weight(uint64_t N, uint64_t K, const s2r_mat* w, const s2r_q8_mat* out,
                          const s2r_q8_mat* out_t, void* stream);
 
-/* Bytes of device workspace that let s2r_q8_gemm cut a long sum among workgroups where the
- * result alone is too small to fill the GPU; 0 where it would not. */
+/* Bytes of device workspace that let s2r_q8_gemm and s2r_q8_gemm_fast cut a long sum among
+ * workgroups where the result alone is too small to fill the GPU; 0 where they would not. */
 size_t s2r_q8_gemm_workspace_bytes(uint64_t M, uint64_t N, uint64_t K);
 
 /* c[m][n] = sum over k < K of value(a[m][k]) * value(b[n][k]).
- * a [M][K] row blocks, b [N][K] square blocks, c [M][N] of any s2r_dtype, rounded once from a
- * sum in fp32.  For a c in fp32 every product is exact and every addition fp32.  For a c in 16
- * bits and M > 32 the products may go through the 8-bit matrix instruction, which adds neighbouring
- * products of a row with about 13 bits below the largest of them: 2.4e-5 of a result's typical
- * size (root mean square, 5001 x 1000 x 4100), where rounding to fp16 costs 2e-4 and to bf16 1.6e-3.
+ * a [M][K] row blocks, b [N][K] square blocks, c [M][N] of any s2r_dtype.  Every product is
+ * exact and every addition fp32; c is rounded once.
  * Layer output: a = X, b = W [N][K].  Input gradient: a = dY, b = the
  * transposed copy of s2r_q8_weight.  Any M from one token up.
  * workspace may be NULL (or ws_bytes 0): the sum is then never cut.  Otherwise it holds at
@@ -109,6 +107,17 @@ size_t s2r_q8_gemm_workspace_bytes(uint64_t M, uint64_t N, uint64_t K);
 s2r_status s2r_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat* a,
                        const s2r_q8_mat* b, const s2r_mat* c, void* workspace, size_t ws_bytes,
                        void* stream);
+
+/* The same call through the 8-bit matrix instruction, about twice as fast for large sizes, for
+ * results that may be a little off: of each eight consecutive k, 8 i .. 8 i + 7, a product is cut
+ * toward zero by less than 2^-13 of the largest of the eight |a b|, where a nonzero value
+ * below its format's normal range (2^-6 of its scale in e4m3, 2^-14 in e5m2) counts as the least
+ * normal.  So a result is off by at most 7 * 2^-13 times the sum of those largest products, apart
+ * from its fp32 additions and its rounding; on ordinary values by 2.4e-5 of its typical size (root mean
+ * square, 5001 x 1000 x 4100).  Few rows of A, which memory bounds, are summed as in s2r_q8_gemm. */
+s2r_status s2r_q8_gemm_fast(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat* a,
+                            const s2r_q8_mat* b, const s2r_mat* c, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /* The same for s2r_q8_wgrad. */
 size_t s2r_q8_wgrad_workspace_bytes(uint64_t M, uint64_t N, uint64_t K);

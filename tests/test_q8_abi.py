@@ -195,3 +195,16 @@ def test_python_descriptors(s2r):
     with pytest.raises(s2r.S2RError) as e:
         s2r.s2r_q8_glu(1, 1, "tanh", m, gq=q, stream=0)
     assert e.value.status == s2r.S2R_ERR_DIM
+
+
+def test_fast_product_refuses_what_the_product_refuses(s2r):
+    L = s2r.lib()
+    a, b, c = _q(s2r), _q(s2r), _m(s2r)
+    bad = [((None, b, c), s2r.S2R_ERR_NULL), ((a, b, None), s2r.S2R_ERR_NULL),
+           ((_q(s2r, q=None), b, c), s2r.S2R_ERR_NULL), ((a, _q(s2r, ld=192), c), s2r.S2R_ERR_DIM),
+           ((_q(s2r, lds=48), b, c), s2r.S2R_ERR_DIM), ((a, b, _m(s2r, dtype=3)), s2r.S2R_ERR_DIM),
+           ((a, b, _m(s2r, data=FAKE + 8)), s2r.S2R_ERR_ALIGN)]
+    for call in (L.s2r_q8_gemm, L.s2r_q8_gemm_fast):
+        for (x, y, z), want in bad:
+            assert call(50, 200, 200, _r(x), _r(y), _r(z), None, 0, None) == want
+        assert call(0, 200, 200, _r(a), _r(b), _r(c), None, 0, None) == s2r.S2R_OK
