@@ -189,16 +189,14 @@ __device__ inline float scale_value(uint32_t b) { return __uint_as_float(b << 23
 
 __device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Magnitude bits of the largest finite of 16 values (as integers fp32 magnitudes order as
-// their values).  The maximum passes over NaN; the instruction takes magnitudes by itself, which
-// the compiler does not use where a value may be a signalling NaN.
+// Magnitude bits of the largest finite of 16 values.  As integers fp32 magnitudes order as their
+// values, with infinity and every NaN above them; a floating maximum would return a quieted
+// signalling NaN and then drop it together with all that came before.
 __device__ inline uint32_t amax16(const float (&x)[16]) {
-  float m = 0;
+  uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < 16; i += 2)
-    asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(m) : "v"(m), "v"(x[i]), "v"(x[i + 1]));
-  uint32_t most = __float_as_uint(m);
-  if (most >= 0x7f800000u) {  // rare: once more, without the infinities
+  for (int i = 0; i < 16; ++i) most = umax(most, __float_as_uint(x[i]) & 0x7fffffffu);
+  if (most >= 0x7f800000u) {  // rare: once more, without infinities and NaN
     most = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

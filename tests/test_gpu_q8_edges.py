@@ -50,3 +50,46 @@ def test_sums_are_fp32_whatever_the_result_is_rounded_to(M, N, K, fa):
     for out in ("f32", "bf16", "f16"):
         for with_ws in (False, True):
             assert torch.equal(q8.gemm(M, N, K, a, b, out, with_ws).double(), want), (out, with_ws)
+
+
+# ---------------------------------------------------------------------------------------
+# NaN with a clear quiet bit
+
+
+SIGNALLING = {"bf16": (torch.int16, [0x7F81, 0x7FBF, -0x7F, -0x41]),  # 0xFF81, 0xFFBF
+              "f16": (torch.int16, [0x7C01, 0x7DFF, -0x3FF, -0x201]),
+              "f32": (torch.int32, [0x7F800001, 0x7FBFFFFF, -0x7FFFFF, -0x400001])}
+
+
+def with_signalling_nan(M, K, dtype):
+    """Every row: a strong element, and behind it one signalling NaN, at every place of a lane."""
+    bits, patterns = SIGNALLING[dtype]
+    x = torch.randn((M, K), generator=q8._gen(4)).to(ref.DTYPES[dtype])
+    for i in range(M):
+        x[i, 0 if i % 2 else (i // 2) % 13] = 300.0 * (-1) ** i
+        x.view(bits)[i, (1 + i // 2) % 16 if i % 2 else 13 + i % 3] = patterns[i % 4]
+        if K > 200:
+            x.view(bits)[i, 128 + (7 * i) % (K - 128)] = patterns[(i + 1) % 4]
+    assert bool(x.isnan().any(1).all())
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_signalling_nan_leaves_its_blocks_scale(fmt, dtype):
+    gp.say(f"signalling NaN {fmt} {dtype}")
+    M, K = 64, 300
+    x = with_signalling_nan(M, K, dtype)
+    out = q8.space(M, K, fmt)
+    s2r.s2r_q8_save(M, K, s2r.mat(q8.wide(M, K, dtype, x=x)), out)
+    q8.check_stored(out, M, K, ref.quantise(x, fmt), fmt)
+    w, w_t = q8.space(M, K, fmt, True), q8.space(K, M, fmt, True)
+    s2r.s2r_q8_weight(M, K, s2r.mat(q8.wide(M, K, dtype, x=x)), w, w_t)
+    q, b = ref.quantise(x, fmt, True)
+    q8.check_stored(w, M, K, (q, b), fmt, True)
+    q8.check_stored(w_t, K, M, (q.t(), b.t()), fmt, True)
+    gq, uq = q8.space(M, K, fmt), q8.space(M, K, fmt)
+    m = s2r.mat(q8.wide(M, K, dtype, x=x)[:, :K])
+    s2r.s2r_q8_glu(M, K, "silu", m, m, gq=gq, uq=uq)
+    q8.check_stored(gq, M, K, ref.quantise(x, fmt), fmt)
+    q8.check_stored(uq, M, K, ref.quantise(x, fmt), fmt)
