@@ -5,15 +5,14 @@
 //   backward  dg = dy u act'(g), du = dy act(g), with g and u as stored
 // act and act' share their transcendental:
 //   SiLU       s = 1 / (1 + e^-g):            act = g s,  act' = s (1 + g (1 - s))
-//   GELU       c = (1 + erf(g / sqrt 2)) / 2: act = g c,  act' = c + g e^(-g^2 / 2) / sqrt(2 pi)
+//   GELU       c = Phi(g):                   act = g c,  act' = c + g e^(-g^2 / 2) / sqrt(2 pi)
 //   GELU_TANH  s = 1 / (1 + e^(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3), which is
 //              (1 + tanh z) / 2:              act = g s,  act' = s + g s (1 - s) 2 z'
 // Element-wise apart from the blocks' largest magnitudes: one read and one write of
 // everything, bound by HBM.  Measured on MI355X: gated SiLU of 8192 x 8192 bf16 with its three 8-bit
 // results 87 us (5.4 TB/s), its gradient 83 us (4.9); with the library's exponential and division the
-// gradient took 97 and was bound by arithmetic.  GELU takes 95 and 113; by the complementary error
-// function, exact far below zero where 1 + erf loses all digits, it took 123 and 146 for values
-// that a block's scale rounds away.
+// gradient took 97 and was bound by arithmetic.  GELU takes 96 and 100; with the library's error
+// function, whose 1 + erf has no digits left far below zero, it took 89 and 108.
 #include "q8_device.hpp"
 #include "q8_launch.hpp"
 
@@ -28,12 +27,14 @@ constexpr int kGluBlocks = 2;  // blocks of 128 columns per workgroup: two or th
 // argument's rounding alone costs |x| half units, and a result next to a border of the 8-bit
 // grid falls to the other side that much more often.  Beyond +-200 it is infinite or zero; a NaN gets
 // lost, but what exp_of's callers multiply it with is the same NaN.
-__device__ inline float exp_of(float x) {
-  x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
+__device__ inline float exp_within_200(float x) {
   const float n = __builtin_rintf(x * 1.44269504088896f);
   float r = __builtin_fmaf(x, 1.44269504088896f, -n);
   r = __builtin_fmaf(x, 1.925963033500e-8f, r);  // log2(e) beyond 24 bits
   return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(r), (int)n);
+}
+__device__ inline float exp_of(float x) {
+  return exp_within_200(__builtin_amdgcn_fmed3f(x, -200.0f, 200.0f));
 }
 
 // The hardware's reciprocal with one step of Newton's.
@@ -42,10 +43,40 @@ __device__ inline float sigmoid(float x) {
   return d < __builtin_inff() ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r;
 }
 
+// Phi(g), the normal distribution's integral, and e = e^(-g^2 / 2).  Phi(-a) = e h(a), where h falls
+// slowly from 1/2 like 1 / (a sqrt(2 pi)) and so keeps all digits however small Phi is: a quotient
+// of polynomials fitted to it over [0, 14.5] in relative error (least squares of the linearised quotient,
+// reweighted by the last quotient's denominator and by Lawson's rule until the error is level:
+// 6e-9), all of its coefficients positive.  The rest of a^2 that its rounding loses comes back by
+// a factor; from a = 14.5 on e is 0 in fp32.  A NaN gets lost as in exp_of.
+__device__ inline float normal_cdf(float g, float& e) {
+  const float a = __builtin_amdgcn_fmed3f(__builtin_fabsf(g), 0.0f, 15.0f);
+  float n = 4.11623903e-3f, d = 1.03177615e-2f;
+  n = __builtin_fmaf(n, a, 4.06327881e-2f);
+  d = __builtin_fmaf(d, a, 1.01857744e-1f);
+  n = __builtin_fmaf(n, a, 1.83233887e-1f);
+  d = __builtin_fmaf(d, a, 4.69467312e-1f);
+  n = __builtin_fmaf(n, a, 4.38293338e-1f);
+  d = __builtin_fmaf(d, a, 1.20249808f);
+  n = __builtin_fmaf(n, a, 0.5f);
+  d = __builtin_fmaf(d, a, 1.67447162f);
+  d = __builtin_fmaf(d, a, 1.0f);
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  const float sq = a * a, rest = __builtin_fmaf(a, a, -sq);
+  e = exp_within_200(-0.5f * sq);
+  e = __builtin_fmaf(-0.5f * e, rest, e);
+  const float tail = e * (n * r);
+  return g < 0 ? tail : 1.0f - tail;
+}
+
 template <int ACT>
 __device__ inline float act_value(float g) {
   if (ACT == S2R_ACT_SILU) return g * sigmoid(g);
-  if (ACT == S2R_ACT_GELU) return g * (0.5f + 0.5f * erff(g * 0.70710678118654752f));
+  if (ACT == S2R_ACT_GELU) {
+    float e;
+    return g * normal_cdf(g, e);
+  }
   const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
   return g * sigmoid(z2);
 }
@@ -57,9 +88,10 @@ __device__ inline void act_both(float g, float& a, float& d) {
     a = g * s;
     d = s * (1.0f + g * (1.0f - s));
   } else if (ACT == S2R_ACT_GELU) {
-    const float c = 0.5f + 0.5f * erff(g * 0.70710678118654752f);
+    float e;
+    const float c = normal_cdf(g, e);
     a = g * c;
-    d = c + g * (exp_of(-0.5f * g * g) * 0.39894228040143268f);
+    d = c + g * (e * 0.39894228040143268f);
   } else {
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float s = sigmoid(z2);

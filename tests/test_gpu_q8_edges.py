@@ -93,3 +93,43 @@ def test_signalling_nan_leaves_its_blocks_scale(fmt, dtype):
     s2r.s2r_q8_glu(M, K, "silu", m, m, gq=gq, uq=uq)
     q8.check_stored(gq, M, K, ref.quantise(x, fmt), fmt)
     q8.check_stored(uq, M, K, ref.quantise(x, fmt), fmt)
+
+
+# ---------------------------------------------------------------------------------------
+# activations
+
+
+def forward(g, kind):
+    """act(g) of a row of fp32 values, in fp32."""
+    n = g.numel()
+    y = q8.wide(1, n, "f32", fill=7.0)
+    s2r.s2r_q8_glu(1, n, kind, s2r.mat(q8.wide(1, n, "f32", x=g[None])[:, :n]), y=s2r.mat(y))
+    return y[0, :n].cpu()
+
+
+def test_gelu_keeps_its_digits_far_below_zero():
+    """g Phi(g) from -13 to 1 against the complementary error function in 64 bits.  Phi(-a) is
+    e^(-a^2 / 2) h(a): the exponential is off by 4 half steps and its correction by 1, h's numerator
+    and denominator by one for each coefficient (5 and 6), their quotient by 3, two more products by 2:
+    21.  Results below fp32's normal range are off by its least number."""
+    gp.say("gelu tail")
+    g = -torch.arange(0, 13 * 512 + 1, dtype=torch.float64) / 512
+    g = torch.cat([g, -g[1:512]]).float()
+    want = ref.act(g.double(), "gelu")[0]
+    got = forward(g, "gelu").double()
+    assert bool(((got - want).abs() <= 21 * HALF * want.abs() + 2.0 ** -148).all())
+
+
+def test_gelu_of_a_block_far_below_zero():
+    """129 columns: the last one is a block of its own, and its scale follows the small value."""
+    gp.say("gelu far block")
+    M, F = 40, 129
+    g = torch.randn((M, F), generator=q8._gen(6))
+    g[:, 128] = -4 - torch.arange(M) / 8
+    yq = q8.space(M, F, "e4m3")
+    s2r.s2r_q8_glu(M, F, "gelu", s2r.mat(q8.wide(M, F, "f32", x=g)[:, :F]), yq=yq)
+    want = ref.act(g.double(), "gelu")[0][:, 128]
+    code = ref.code_values("e4m3")[yq.codes[:, 128].cpu().int()]
+    got = code * torch.exp2(yq.scales[1, :M].cpu().double() - 127)
+    # half a step of e4m3, and the value's own error, far below what is left
+    assert bool(((got - want).abs() <= 1.001 * 2.0 ** -4 * want.abs()).all())
