@@ -70,6 +70,14 @@ __device__ inline float normal_cdf(float g, float& e) {
   return g < 0 ? tail : 1.0f - tail;
 }
 
+// 2 z of GELU_TANH, and cubic = 0.044715 g^2.  g^2 is taken no further than 16^2, where the sigmoid
+// has long been 0 or 1: an infinite one would meet s (1 - s) = 0 in the derivative.
+__device__ inline float tanh_argument(float g, float& cubic) {
+  const float h = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f);
+  cubic = 0.044715f * h * h;
+  return 1.5957691216057308f * g * (1.0f + cubic);
+}
+
 template <int ACT>
 __device__ inline float act_value(float g) {
   if (ACT == S2R_ACT_SILU) return g * sigmoid(g);
@@ -77,8 +85,8 @@ __device__ inline float act_value(float g) {
     float e;
     return g * normal_cdf(g, e);
   }
-  const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return g * sigmoid(z2);
+  float cubic;
+  return g * sigmoid(tanh_argument(g, cubic));
 }
 
 template <int ACT>
@@ -93,10 +101,10 @@ __device__ inline void act_both(float g, float& a, float& d) {
     a = g * c;
     d = c + g * (e * 0.39894228040143268f);
   } else {
-    const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
-    const float s = sigmoid(z2);
+    float cubic;
+    const float s = sigmoid(tanh_argument(g, cubic));
     a = g * s;
-    d = s + a * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * g * g));
+    d = s + a * (1.0f - s) * (1.5957691216057308f * (1.0f + 3.0f * cubic));
   }
 }
 

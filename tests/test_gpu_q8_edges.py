@@ -107,6 +107,26 @@ def forward(g, kind):
     return y[0, :n].cpu()
 
 
+def derivative(v):
+    """(stored values in fp64, function that gives act' of them in fp32) for a row of multiples of a
+    code's step."""
+    m, values = v
+    n = values.shape[1]
+
+    def of(kind):
+        one, d = torch.ones((1, ref.up(n, 8)), device=DEV), q8.wide(1, n, "f32", fill=7.0)
+        s2r.s2r_q8_glu_grad(1, n, kind, m, None, s2r.mat(one), dg=s2r.mat(d))
+        return d[0, :n].cpu().double()
+    return values[0], of
+
+
+def codes_of(values, byte=127, fmt="e4m3"):
+    c = (values / 2.0 ** (byte - 127)).float().to(ref.F8[fmt])
+    blocks = ref.up(len(values), 128) // 128
+    m = q8.stored(c.view(torch.uint8)[None], torch.full((1, blocks), byte), fmt)
+    return m, c.double()[None] * 2.0 ** (byte - 127)
+
+
 def test_gelu_keeps_its_digits_far_below_zero():
     """g Phi(g) from -13 to 1 against the complementary error function in 64 bits.  Phi(-a) is
     e^(-a^2 / 2) h(a): the exponential is off by 4 half steps and its correction by 1, h's numerator
@@ -133,3 +153,13 @@ def test_gelu_of_a_block_far_below_zero():
     got = code * torch.exp2(yq.scales[1, :M].cpu().double() - 127)
     # half a step of e4m3, and the value's own error, far below what is left
     assert bool(((got - want).abs() <= 1.001 * 2.0 ** -4 * want.abs()).all())
+
+
+@pytest.mark.parametrize("kind", q8.ACTS)
+def test_derivative_of_huge_values(kind):
+    """0 on the left and 1 on the right, up to the largest that a stored matrix holds."""
+    gp.say(f"derivative of huge values {kind}")
+    for byte in (127, 160, 187, 190, 220, 239):
+        v = torch.tensor([-448.0, -256.0, 256.0, 448.0], dtype=torch.float64) * 2.0 ** (byte - 127)
+        values, of = derivative(codes_of(v, byte))
+        assert of(kind).abs().tolist() == [0.0, 0.0, 1.0, 1.0], byte
