@@ -4,10 +4,10 @@
 //   forward   y = act(g) u;  g, u and y leave in 8 bits (and y in 16 or 32 if asked)
 //   backward  dg = dy u act'(g), du = dy act(g), with g and u as stored
 // act and act' share their transcendental:
-//   SiLU       s = 1 / (1 + e^-g):            act = g s,  act' = s (1 + g (1 - s))
+//   SiLU       s = 1 / (1 + e^-g):           act = g s,  act' = s (1 + g (1 - s))
 //   GELU       c = Phi(g):                   act = g c,  act' = c + g e^(-g^2 / 2) / sqrt(2 pi)
 //   GELU_TANH  s = 1 / (1 + e^(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3), which is
-//              (1 + tanh z) / 2:              act = g s,  act' = s + g s (1 - s) 2 z'
+//              (1 + tanh z) / 2:             act = g s,  act' = s + g s (1 - s) 2 z'
 // Element-wise apart from the blocks' largest magnitudes: one read and one write of
 // everything, bound by HBM.  Measured on MI355X: gated SiLU of 8192 x 8192 bf16 with its three 8-bit
 // results 87 us (5.4 TB/s), its gradient 83 us (4.9); with the library's exponential and division the
@@ -37,10 +37,14 @@ __device__ inline float exp_of(float x) {
   return exp_within_200(__builtin_amdgcn_fmed3f(x, -200.0f, 200.0f));
 }
 
-// The hardware's reciprocal with one step of Newton's.
-__device__ inline float sigmoid(float x) {
-  const float d = 1.0f + exp_of(-x), r = __builtin_amdgcn_rcpf(d);
-  return d < __builtin_inff() ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r;
+// s = 1 / (1 + e^-x) by the hardware's reciprocal with one step of Newton's, and 1 - s as e^-x s: where s
+// is near 1 the subtraction would leave few digits.
+__device__ inline float sigmoid(float x, float& rest) {
+  const float e = exp_of(-x), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+  const bool finite = d < __builtin_inff();
+  const float s = finite ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r;
+  rest = finite ? e * s : 1.0f;
+  return s;
 }
 
 // Phi(g), the normal distribution's integral, and e = e^(-g^2 / 2).  Phi(-a) = e h(a), where h falls
@@ -80,31 +84,33 @@ __device__ inline float tanh_argument(float g, float& cubic) {
 
 template <int ACT>
 __device__ inline float act_value(float g) {
-  if (ACT == S2R_ACT_SILU) return g * sigmoid(g);
+  float rest;
+  if (ACT == S2R_ACT_SILU) return g * sigmoid(g, rest);
   if (ACT == S2R_ACT_GELU) {
     float e;
     return g * normal_cdf(g, e);
   }
   float cubic;
-  return g * sigmoid(tanh_argument(g, cubic));
+  return g * sigmoid(tanh_argument(g, cubic), rest);
 }
 
 template <int ACT>
 __device__ inline void act_both(float g, float& a, float& d) {
   if (ACT == S2R_ACT_SILU) {
-    const float s = sigmoid(g);
+    float rest;
+    const float s = sigmoid(g, rest);
     a = g * s;
-    d = s * (1.0f + g * (1.0f - s));
+    d = s * (1.0f + g * rest);
   } else if (ACT == S2R_ACT_GELU) {
     float e;
     const float c = normal_cdf(g, e);
     a = g * c;
     d = c + g * (e * 0.39894228040143268f);
   } else {
-    float cubic;
-    const float s = sigmoid(tanh_argument(g, cubic));
+    float cubic, rest;
+    const float s = sigmoid(tanh_argument(g, cubic), rest);
     a = g * s;
-    d = s + a * (1.0f - s) * (1.5957691216057308f * (1.0f + 3.0f * cubic));
+    d = s + a * rest * (1.5957691216057308f * (1.0f + 3.0f * cubic));
   }
 }
 

@@ -155,6 +155,22 @@ def test_gelu_of_a_block_far_below_zero():
     assert bool(((got - want).abs() <= 1.001 * 2.0 ** -4 * want.abs()).all())
 
 
+@pytest.mark.parametrize("kind,lo,hi", [("silu", 4, 17), ("gelu_tanh", 3, 8)])
+def test_derivative_keeps_its_digits_where_the_sigmoid_is_near_one(kind, lo, hi):
+    """act' = s plus a small term, s = 1 / (1 + e) with e below 0.02.  In half steps: the sum 1 + e and its
+    reciprocal 1 each, e's own error (4, for the tanh form 31 with its argument's) times e below
+    0.1; the small term, below 0.08 and off by 9 (tanh form: below 0.02 and off by 40), below 0.8;
+    the last sum and product 1 each, and what is of second order: below 6."""
+    gp.say(f"derivative near one {kind}")
+    v = torch.cat([torch.arange(8, 16).double() / 8 * 2.0 ** e for e in range(1, 5)])
+    v = v[(v >= lo) & (v <= hi)]
+    values, of = derivative(codes_of(v))
+    want = ref.act(values, kind)[1]
+    assert len(values) > 10
+    got = of(kind)
+    assert bool(((got - want).abs() <= 6 * HALF * want.abs()).all()), ((got - want) / want / HALF)
+
+
 @pytest.mark.parametrize("kind", q8.ACTS)
 def test_derivative_of_huge_values(kind):
     """0 on the left and 1 on the right, up to the largest that a stored matrix holds."""
