@@ -234,12 +234,23 @@ __device__ inline uint32_t encode4(float a, float b, float c, float d, float sca
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// 16 values to codes under the scale byte sb.  The largest scale is that of blocks with values next to
+// fp32's largest, some of which round to 2^128: that is code 0x78 in both formats, and the
+// code below it is within a step of them too.
 template <int FMT>
-__device__ inline u32x4 encode16(const float (&x)[16], float scale) {
+__device__ inline u32x4 encode16(const float (&x)[16], uint32_t sb) {
+  const float scale = scale_value(sb);
   u32x4 q;
 #pragma unroll
   for (int w = 0; w < 4; ++w)
     q[w] = encode4<FMT>(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3], scale);
+  if (sb == 255 - scale_bias<FMT>()) {  // rare
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t off = (q[w] & 0x7f7f7f7fu) ^ 0x78787878u;  // 0 in the bytes meant
+      q[w] -= (~(off + 0x7f7f7f7fu) & 0x80808080u) >> 7;
+    }
+  }
   return q;
 }
 

@@ -122,10 +122,10 @@ __device__ inline void put8(const s2r_q8_mat& o, uint32_t m, uint32_t c, uint32_
   u32x4 code;
   if (o.format == S2R_E4M3) {
     sb = scale_byte<S2R_E4M3>(am);
-    code = encode16<S2R_E4M3>(v, scale_value(sb));
+    code = encode16<S2R_E4M3>(v, sb);
   } else {
     sb = scale_byte<S2R_E5M2>(am);
-    code = encode16<S2R_E5M2>(v, scale_value(sb));
+    code = encode16<S2R_E5M2>(v, sb);
   }
   if (c >= F) return;
   store_codes16(o.q + (uint64_t)m * o.ld, c, F, code);

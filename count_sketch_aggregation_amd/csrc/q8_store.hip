@@ -35,7 +35,7 @@ __global__ __launch_bounds__(kStoreThreads) void k_q8_save(
     float v[16];
     unpack16<DT>(r[b], v);
     const uint32_t sb = scale_byte<FMT>(max_over_8(amax16(v)));
-    if (c < K) store_codes16(qrow, c, K, encode16<FMT>(v, scale_value(sb)));
+    if (c < K) store_codes16(qrow, c, K, encode16<FMT>(v, sb));
     if (threadIdx.x % 8 == 0 && c < K) scale[(uint64_t)(c / kQ8Block) * lds + m] = (uint8_t)sb;
   }
 }
@@ -140,13 +140,12 @@ __global__ __launch_bounds__(kStoreThreads) void k_q8_weight(
     scale[(uint64_t)kb * lds + nb] = (uint8_t)sb;
     if (qt) scale_t[(uint64_t)nb * ldst + kb] = (uint8_t)sb;
   }
-  const float scale_f = scale_value(sb);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t rr = t / 8 + 32 * i, n = nb * kQ8Block + rr;
     float v[16];
     unpack16<DT>(r[i], v);
-    const u32x4 code = encode16<FMT>(v, scale_f);
+    const u32x4 code = encode16<FMT>(v, sb);
     if (n < N && c < K) store_codes16(q + (uint64_t)n * ldq, c, K, code);
     if (qt) {
 #pragma unroll

@@ -27,7 +27,9 @@
  * 2^-3 (e5m2) of itself, or by 2^-10 (e4m3) or 2^-17 (e5m2) of its block's scale if it is
  * below the format's normal range.  NaN stays NaN; an infinity becomes NaN in e4m3 and stays
  * in e5m2; neither changes the scale of its block.  Every stored value is exact in bf16 and
- * in fp32.  Scale bytes of matrices written elsewhere must be 17 .. 240.
+ * in fp32, and finite if it was: what would round to 2^128 gets the largest code below it, within
+ * the same bounds.  Scale bytes are 17 .. 247 (e4m3) or 17 .. 240 (e5m2), also those of
+ * matrices written elsewhere, whose values must be below 2^128.
  *
  * Conventions, beyond those of s2r.h (device memory, streams, host checks before anything is
  * enqueued, no allocation, calls from several threads):

@@ -179,3 +179,53 @@ def test_derivative_of_huge_values(kind):
         v = torch.tensor([-448.0, -256.0, 256.0, 448.0], dtype=torch.float64) * 2.0 ** (byte - 127)
         values, of = derivative(codes_of(v, byte))
         assert of(kind).abs().tolist() == [0.0, 0.0, 1.0, 1.0], byte
+
+
+# ---------------------------------------------------------------------------------------
+# the ends of the range
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_next_to_the_largest_stay_finite(dtype, fmt):
+    """What would round to 2^128 is stored as the largest code below it: still off by at most
+    2^-4 (e4m3) or 2^-3 (e5m2) of itself, and finite in bf16 and fp32.  Infinities and NaN stay."""
+    gp.say(f"largest values {dtype} {fmt}")
+    M, K = 9, 300
+    top = {"bf16": 255 * 2.0 ** 120, "f32": (2 - 2.0 ** -23) * 2.0 ** 127}[dtype]
+    f = torch.linspace(0.8, 1.0, M * K, dtype=torch.float64).reshape(M, K) * top
+    f[:, ::3] *= -1
+    f[0, 3] = f[1, 0] = top
+    f[2, 0] = -top
+    f[3, :200] = torch.linspace(-1, 1, 200) * 1e30
+    f[4, 7], f[5, 8], f[6, 9] = math.inf, -math.inf, math.nan
+    x = f.to(ref.DTYPES[dtype])
+    fin = torch.isfinite(x)
+    want = x.double()
+    share = 2.0 ** -4 if fmt == "e4m3" else 2.0 ** -3
+    least = 2.0 ** -10 if fmt == "e4m3" else 2.0 ** -17  # below the format's normal range, times the scale
+
+    def check(m, rows, cols, back, square):
+        got = back.double()
+        ok = torch.isfinite(got)
+        assert bool(ok[fin].all()) and not bool(ok[~fin].any())
+        b = m.scales.cpu().double() - 127
+        s = torch.exp2(b[:ref.up(cols, 128) // 128]).t()
+        s = (s[:1].expand(rows, -1) if square else s[:rows]).repeat_interleave(128, 1)[:, :cols]
+        off = (got - want)[fin].abs()
+        assert bool((off <= torch.maximum(share * want[fin].abs(), least * s[fin])).all())
+
+    out = q8.space(M, K, fmt)
+    s2r.s2r_q8_save(M, K, s2r.mat(q8.wide(M, K, dtype, x=x)), out)
+    for t in ("f32", "bf16"):
+        y = q8.wide(M, K, t, fill=7.0)
+        s2r.s2r_q8_load(M, K, out, s2r.mat(y))
+        check(out, M, K, y[:, :K].cpu(), False)
+    gq = q8.space(M, K, fmt)
+    s2r.s2r_q8_glu(M, K, "silu", s2r.mat(q8.wide(M, K, dtype, x=x)[:, :K]), gq=gq)
+    assert torch.equal(gq.codes, out.codes) and torch.equal(gq.scales, out.scales)
+    w = q8.space(M, K, fmt, True)
+    s2r.s2r_q8_weight(M, K, s2r.mat(q8.wide(M, K, dtype, x=x)), w)
+    code = ref.code_values(fmt)[w.codes[:, :K].cpu().int()]
+    scale = torch.exp2(w.scales[:, 0].cpu().double() - 127).repeat_interleave(128)[:K]
+    check(w, M, K, (code * scale).float(), True)
