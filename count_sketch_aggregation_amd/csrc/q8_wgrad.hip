@@ -69,11 +69,12 @@ struct Feed {
   __device__ __amdgpu_buffer_rsrc_t view() const { return rsrc_of(base, left); }
   // The compiler would have every transposing load of LDS wait for every load that is on its
   // way there: it is not told of these, and the loop waits for them itself.  Nothing comes back
-  // to a register; the pause covers scalar registers that a vector instruction has just written.
+  // to a register; m0, the place in LDS, is an input, so that the compiler knows what it holds; the
+  // pause covers it and scalar registers that a vector instruction has just written.
   __device__ void load(uint32_t lds, u32x4 v, int j) const {
     const uint32_t to = lds + (wave * kLoads + j) * 1024;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at[j]), "s"(v) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(at[j]), "s"(v), "{m0}"(__builtin_amdgcn_readfirstlane(to)) : "memory");
   }
   __device__ u32x4 words() const {
     const uint32_t n = left > 0xc0000000ull ? 0xc0000000u : (uint32_t)left;
