@@ -285,16 +285,20 @@ hipError_t launch_q8_glu(uint64_t M, uint64_t F, s2r_act act, const s2r_mat& g, 
                          const s2r_q8_mat* gq, const s2r_q8_mat* uq, const s2r_mat* y,
                          const s2r_q8_mat* yq, hipStream_t s) {
   const uint32_t ct = (uint32_t)((F + kGluBlocks * kQ8Block - 1) / (kGluBlocks * kQ8Block));
-  const uint32_t grid = (uint32_t)((M + kGluRows - 1) / kGluRows * ct);
-  const s2r_q8_mat a = or_none(gq), b = or_none(uq), c = or_none(yq);
-  const s2r_mat d = or_none(y);
   trace_mark(s, "k_q8_glu");
-  if (g.dtype == S2R_BF16)
-    S2R_Q8_ACT(act, (go_glu<S2R_BF16, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
-  else if (g.dtype == S2R_F16)
-    S2R_Q8_ACT(act, (go_glu<S2R_F16, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
-  else
-    S2R_Q8_ACT(act, (go_glu<S2R_F32, ACT>(grid, s, M, F, ct, g, u, a, b, d, c)));
+  by_rows(M, kGluRows, ct, [&](uint64_t m, uint64_t rows) {
+    const uint32_t grid = (uint32_t)((rows + kGluRows - 1) / kGluRows * ct);
+    const s2r_mat from = from_row(g, m), up = from_row(or_none(u), m), d = from_row(or_none(y), m);
+    const s2r_mat* const gate = u ? &up : nullptr;
+    const s2r_q8_mat a = from_row(or_none(gq), m), b = from_row(or_none(uq), m),
+                     c = from_row(or_none(yq), m);
+    if (g.dtype == S2R_BF16)
+      S2R_Q8_ACT(act, (go_glu<S2R_BF16, ACT>(grid, s, rows, F, ct, from, gate, a, b, d, c)));
+    else if (g.dtype == S2R_F16)
+      S2R_Q8_ACT(act, (go_glu<S2R_F16, ACT>(grid, s, rows, F, ct, from, gate, a, b, d, c)));
+    else
+      S2R_Q8_ACT(act, (go_glu<S2R_F32, ACT>(grid, s, rows, F, ct, from, gate, a, b, d, c)));
+  });
   return hipGetLastError();
 }
 
@@ -303,14 +307,18 @@ hipError_t launch_q8_glu_grad(uint64_t M, uint64_t F, s2r_act act, const s2r_q8_
                               const s2r_mat* du, const s2r_q8_mat* dgq, const s2r_q8_mat* duq,
                               hipStream_t s) {
   const uint32_t ct = (uint32_t)((F + kGluBlocks * kQ8Block - 1) / (kGluBlocks * kQ8Block));
-  const uint32_t grid = (uint32_t)((M + kGluRows - 1) / kGluRows * ct);
-  const s2r_mat a = or_none(dg), b = or_none(du);
-  const s2r_q8_mat c = or_none(dgq), d = or_none(duq);
   trace_mark(s, "k_q8_glu_grad");
-  if (gq.format == S2R_E4M3)
-    S2R_Q8_ACT(act, (go_grad<S2R_E4M3, ACT>(grid, s, M, F, ct, gq, uq, dy, a, b, c, d)));
-  else
-    S2R_Q8_ACT(act, (go_grad<S2R_E5M2, ACT>(grid, s, M, F, ct, gq, uq, dy, a, b, c, d)));
+  by_rows(M, kGluRows, ct, [&](uint64_t m, uint64_t rows) {
+    const uint32_t grid = (uint32_t)((rows + kGluRows - 1) / kGluRows * ct);
+    const s2r_q8_mat from = from_row(gq, m), up = from_row(or_none(uq), m);
+    const s2r_q8_mat* const gate = uq ? &up : nullptr;
+    const s2r_mat dym = from_row(dy, m), a = from_row(or_none(dg), m), b = from_row(or_none(du), m);
+    const s2r_q8_mat c = from_row(or_none(dgq), m), d = from_row(or_none(duq), m);
+    if (gq.format == S2R_E4M3)
+      S2R_Q8_ACT(act, (go_grad<S2R_E4M3, ACT>(grid, s, rows, F, ct, from, gate, dym, a, b, c, d)));
+    else
+      S2R_Q8_ACT(act, (go_grad<S2R_E5M2, ACT>(grid, s, rows, F, ct, from, gate, dym, a, b, c, d)));
+  });
   return hipGetLastError();
 }
 

@@ -191,24 +191,33 @@ __global__ __launch_bounds__(kStoreThreads) void k_q8_weight(
 hipError_t launch_q8_save(uint64_t M, uint64_t K, const s2r_mat& x, const s2r_q8_mat& out,
                           hipStream_t s) {
   const uint64_t ct = (K + kStoreBlocks * kQ8Block - 1) / (kStoreBlocks * kQ8Block);
-  const uint64_t rt = (M + kStoreRows - 1) / kStoreRows;
   trace_mark(s, "k_q8_save");
-  S2R_Q8_DISPATCH(x.dtype, out.format,
-                  hipLaunchKernelGGL((k_q8_save<DT, FMT>), dim3((uint32_t)(ct * rt)),
-                                     dim3(kStoreThreads), 0, s, x.data, x.ld, out.q, out.ld,
-                                     out.scale, out.lds, (uint32_t)M, (uint32_t)K, (uint32_t)ct));
+  by_rows(M, kStoreRows, ct, [&](uint64_t m, uint64_t rows) {
+    const s2r_mat f = from_row(x, m);
+    const s2r_q8_mat t = from_row(out, m);
+    const uint32_t grid = (uint32_t)(ct * ((rows + kStoreRows - 1) / kStoreRows));
+    S2R_Q8_DISPATCH(x.dtype, out.format,
+                    hipLaunchKernelGGL((k_q8_save<DT, FMT>), dim3(grid), dim3(kStoreThreads), 0, s,
+                                       f.data, f.ld, t.q, t.ld, t.scale, t.lds, (uint32_t)rows,
+                                       (uint32_t)K, (uint32_t)ct));
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_q8_load(uint64_t M, uint64_t K, const s2r_q8_mat& in, const s2r_mat& x,
                           hipStream_t s) {
-  const uint64_t cols = 1024 / (x.dtype == S2R_F32 ? 4 : 2), rows = kStoreThreads / 64 * kLoadRows;
-  const uint64_t ct = (K + cols - 1) / cols, rt = (M + rows - 1) / rows;
+  const uint64_t cols = 1024 / (x.dtype == S2R_F32 ? 4 : 2), each = kStoreThreads / 64 * kLoadRows;
+  const uint64_t ct = (K + cols - 1) / cols;
   trace_mark(s, "k_q8_load");
-  S2R_Q8_DISPATCH(x.dtype, in.format,
-                  hipLaunchKernelGGL((k_q8_load<DT, FMT>), dim3((uint32_t)(ct * rt)),
-                                     dim3(kStoreThreads), 0, s, in.q, in.ld, in.scale, in.lds,
-                                     x.data, x.ld, (uint32_t)M, (uint32_t)K, (uint32_t)ct));
+  by_rows(M, each, ct, [&](uint64_t m, uint64_t rows) {
+    const s2r_q8_mat f = from_row(in, m);
+    const s2r_mat t = from_row(x, m);
+    const uint32_t grid = (uint32_t)(ct * ((rows + each - 1) / each));
+    S2R_Q8_DISPATCH(x.dtype, in.format,
+                    hipLaunchKernelGGL((k_q8_load<DT, FMT>), dim3(grid), dim3(kStoreThreads), 0, s,
+                                       f.q, f.ld, f.scale, f.lds, t.data, t.ld, (uint32_t)rows,
+                                       (uint32_t)K, (uint32_t)ct));
+  });
   return hipGetLastError();
 }
 

@@ -229,3 +229,23 @@ def test_values_next_to_the_largest_stay_finite(dtype, fmt):
     code = ref.code_values(fmt)[w.codes[:, :K].cpu().int()]
     scale = torch.exp2(w.scales[:, 0].cpu().double() - 127).repeat_interleave(128)[:K]
     check(w, M, K, (code * scale).float(), True)
+
+
+def test_the_most_rows():
+    """2^28 - 1 rows: more workgroups than one launch holds."""
+    gp.say("most rows")
+    M, K = (1 << 28) - 1, 16
+    x = torch.randint(0, 256, (M, K), dtype=torch.uint8, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+    x[x.bitwise_and(0x7F) == 0x7F] = 0
+    m = s2r.q8_mat(x, torch.full((1, 1 << 28), 127, dtype=torch.uint8, device=DEV))
+    y = torch.full((M, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    s2r.s2r_q8_load(M, K, m, s2r.mat(y))
+    half = 1 << 27
+    for part in (slice(0, half), slice(half, M)):
+        assert torch.equal(y[part], x[part].view(torch.float8_e4m3fn).bfloat16())
+    back = s2r.alloc_q8(M, K)
+    s2r.s2r_q8_save(M, K, s2r.mat(y), back)
+    again = torch.empty_like(y)
+    s2r.s2r_q8_load(M, K, back, s2r.mat(again))
+    for part in (slice(0, half), slice(half, M)):  # a smaller scale holds every value too
+        assert torch.equal(again[part], y[part])
