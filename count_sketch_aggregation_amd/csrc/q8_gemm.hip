@@ -178,7 +178,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
   }
 
   // The stream of blocks: the newest that is loaded, and the first one of the item after its
-  // own.  Rows beyond M and N lie beyond the views' ends.
+  // own.  The views end with the last row's last 16-byte piece.
+  const uint32_t row_end = (K + 15) / 16 * 16;
   struct At {
     uint32_t item, left;  // blocks of the item after this one
     uint64_t a, b, len_a, len_b, scale_a;
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     x.left = __builtin_amdgcn_readfirstlane(min(block + part_blocks, blocks) - block - 1);
     x.a = (uint64_t)a.q + (uint64_t)m0 * a.ld + k;
     x.b = (uint64_t)b.q + (uint64_t)n0 * b.ld + k;
-    x.len_a = (uint64_t)(M - m0) * a.ld - k;
-    x.len_b = (uint64_t)(N - n0) * b.ld - k;
+    x.len_a = (uint64_t)(M - m0 - 1) * a.ld + row_end - k;
+    x.len_b = (uint64_t)(N - n0 - 1) * b.ld + row_end - k;
     x.scale_a += block * a.lds;
     x.scale_b += block * b.lds + min(n0 + wn, N - 1) / kQ8Block;
     x.lane_scale = min(m0 + wm + FM * r, (uint32_t)a.lds - FM);

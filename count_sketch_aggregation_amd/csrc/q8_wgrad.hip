@@ -46,8 +46,8 @@ struct Feed {
     const uint64_t skip = kDirect ? 2 * (uint64_t)c0 : c0;
     wave = w;
     base = (kDirect ? (uint64_t)m.data : (uint64_t)q.q) + (uint64_t)first * ld + skip;
-    const uint64_t all = (uint64_t)(end - first) * ld;
-    left = all > skip ? all - skip : 0;
+    const uint32_t row_end = (cols * (kDirect ? 2 : 1) + 15) / 16 * 16;  // of the last row's last piece
+    left = (uint64_t)(end - first - 1) * ld + row_end - skip;
     step = (uint64_t)kWgradRows * ld;
     const uint32_t p0 = wave * (kLoads * kRows) + r;
 #pragma unroll

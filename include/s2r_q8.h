@@ -36,9 +36,11 @@
  *   - Matrices are row-major with unit stride along a row.  q, scale and every s2r_mat are
  *     described by the host structs below, copied at call time.
  *   - Alignment: q and data 16 bytes, ld a multiple of 16 bytes (ld % 16 for codes, % 8 for
- *     16-bit and % 4 for fp32 elements); scale 4 bytes and lds % 4 == 0.  A buffer holds whole
- *     rows: the elements between a row's last column and ld exist, are never written, and
- *     may hold anything.
+ *     16-bit and % 4 for fp32 elements); scale 4 bytes and lds % 4 == 0.  The elements after
+ *     a row's last column up to a multiple of 16 bytes exist, are never written, and may hold
+ *     anything; nothing beyond them is touched.  So a matrix may be a range of columns of a
+ *     wider one (of 8-bit ones from a multiple of 128 on, with the scales of its blocks), and two
+ *     products that add up, as dX = dG Wg + dU Wu, are one of matrices side by side.
  *   - Sizes: rows and columns below 2^28; ld of at most 2^22 elements.  A size of 0 is a call
  *     that writes nothing, but an empty sum is a sum: K == 0 in s2r_q8_gemm writes zeros, and
  *     M == 0 in s2r_q8_wgrad without `accumulate` too.

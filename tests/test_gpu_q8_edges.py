@@ -249,3 +249,71 @@ def test_the_most_rows():
     s2r.s2r_q8_load(M, K, back, s2r.mat(again))
     for part in (slice(0, half), slice(half, M)):  # a smaller scale holds every value too
         assert torch.equal(again[part], y[part])
+
+
+# ---------------------------------------------------------------------------------------
+# ranges of columns
+
+
+def columns(m, first, last):
+    """Columns first .. last - 1 of an 8-bit matrix, first a multiple of 128."""
+    fmt = ["e4m3", "e5m2"][m.format]
+    return s2r.q8_mat(m.codes[:, first:last], m.scales[first // 128:ref.up(last, 128) // 128], fmt)
+
+
+@pytest.mark.parametrize("M,F,D", [(7, 128, 100), (131, 384, 260), (700, 256, 500)])
+def test_matrices_side_by_side(M, F, D):
+    """A gated layer whose g and u, their checkpoints, their gradients and its weights' transposes
+    each lie in one matrix of 2 F columns, the last of which ends the buffer: the same bits as apart, and
+    the input gradient dg Wg + du Wu is one product over both halves."""
+    gp.say(f"side by side {M}x{F}x{D}")
+    g = q8._gen(3)
+    bf = lambda r, c: (torch.randn((r, c), generator=g)).bfloat16().to(DEV)
+    h, x, dy = bf(M, 2 * F), bf(M, ref.up(D, 8)), bf(M, F)
+    halves = lambda t: (s2r.mat(t[:, :F]), s2r.mat(t[:, F:]))
+    new = lambda r, c, **k: s2r.alloc_q8(r, c, **k)
+    both, grads = new(M, 2 * F), new(M, 2 * F, fmt="e5m2")
+    split = lambda m: (columns(m, 0, F), columns(m, F, 2 * F))
+    s2r.s2r_q8_glu(M, F, "silu", *halves(h), gq=split(both)[0], uq=split(both)[1])
+    s2r.s2r_q8_glu_grad(M, F, "silu", *split(both), s2r.mat(dy), dgq=split(grads)[0], duq=split(grads)[1])
+    apart, apart_grads = [new(M, F) for _ in range(2)], [new(M, F, fmt="e5m2") for _ in range(2)]
+    s2r.s2r_q8_glu(M, F, "silu", s2r.mat(h[:, :F].contiguous()), s2r.mat(h[:, F:].contiguous()), gq=apart[0], uq=apart[1])
+    s2r.s2r_q8_glu_grad(M, F, "silu", *apart, s2r.mat(dy), dgq=apart_grads[0], duq=apart_grads[1])
+    for m, parts in ((both, apart), (grads, apart_grads)):
+        for half, part in zip(split(m), parts):
+            assert torch.equal(half.codes, part.codes) and torch.equal(half.scales[:, :M], part.scales[:, :M])
+    # weight gradients from halves: codes, and a bf16 range that ends its buffer
+    xq = new(M, D)
+    s2r.s2r_q8_save(M, D, s2r.mat(x), xq)
+    for i in range(2):
+        for one, two in ((split(grads)[i], apart_grads[i]), (halves(h)[i], s2r.mat(h[:, i * F:(i + 1) * F].contiguous()))):
+            dw = [torch.zeros((F, D), device=DEV) for _ in range(2)]
+            s2r.s2r_q8_wgrad(M, F, D, one, xq, dw[0], D)
+            s2r.s2r_q8_wgrad(M, F, D, two, xq, dw[1], D)
+            assert torch.equal(*dw)
+    # the input gradient
+    w = [torch.randn((F, D), generator=g).to(DEV) / 16 for _ in range(2)]
+    wq, wt = [new(F, D, square=True) for _ in range(2)], new(D, 2 * F, square=True)
+    for i in range(2):
+        padded = torch.zeros((F, ref.up(D, 4)), device=DEV)
+        padded[:, :D] = w[i]
+        s2r.s2r_q8_weight(F, D, s2r.mat(padded), wq[i], split(wt)[i])
+    dx = q8.wide(M, D, "f32", fill=7.0)
+    s2r.s2r_q8_gemm(M, D, 2 * F, grads, wt, s2r.mat(dx))
+    value = lambda m, r, c, square: ref.code_values(["e4m3", "e5m2"][m.format])[m.codes[:, :c].cpu().int()] * ref.spread(
+        m.scales.cpu().t().long()[:ref.up(r, 128) // 128 if square else r], r, c, square)
+    dv, wv = value(grads, M, 2 * F, False), value(wt, D, 2 * F, True)
+    want, mass = dv @ wv.t(), dv.abs() @ wv.abs().t()
+    assert bool(((dx[:, :D].cpu().double() - want).abs() <= 2 * F * 2.0 ** -23 * mass).all())
+    want_w = torch.cat([(ref.quantise(t.cpu(), "e4m3", True)[0] * ref.spread(ref.quantise(t.cpu(), "e4m3", True)[1], F, D, True)).t()
+                        for t in w], 1)
+    assert torch.equal(wv, want_w)
+    # each half alone, the second one ending its buffer
+    for i in range(2):
+        y = [q8.wide(M, D, "f32", fill=7.0) for _ in range(2)]
+        s2r.s2r_q8_gemm(M, D, F, split(grads)[i], split(wt)[i], s2r.mat(y[0]))
+        wti = new(D, F, square=True)
+        wti.codes.copy_(split(wt)[i].codes)
+        wti.scales.copy_(split(wt)[i].scales)
+        s2r.s2r_q8_gemm(M, D, F, apart_grads[i], wti, s2r.mat(y[1]))
+        assert torch.equal(y[0][:, :D], y[1][:, :D])
