@@ -208,3 +208,26 @@ def test_fast_product_refuses_what_the_product_refuses(s2r):
         for (x, y, z), want in bad:
             assert call(50, 200, 200, _r(x), _r(y), _r(z), None, 0, None) == want
         assert call(0, 200, 200, _r(a), _r(b), _r(c), None, 0, None) == s2r.S2R_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(129, 127, 4100), (64, 8192, 4100)])
+def test_a_products_workspace_is_checked(s2r, M, N, K):
+    """Sizes whose sum is cut: too small and misaligned workspaces are refused, by both products."""
+    L = s2r.lib()
+    need = s2r.s2r_q8_gemm_workspace_bytes(M, N, K)
+    assert need > 0 and need % (4 * M) == 0
+    a, b, c = _q(s2r, ld=4112, lds=256), _q(s2r, ld=4112, lds=64), _m(s2r, ld=8192)
+    for call in (L.s2r_q8_gemm, L.s2r_q8_gemm_fast):
+        assert call(M, N, K, _r(a), _r(b), _r(c), FAKE, need - 1, None) == s2r.S2R_ERR_WORKSPACE
+        assert call(M, N, K, _r(a), _r(b), _r(c), FAKE, 1, None) == s2r.S2R_ERR_WORKSPACE
+        assert call(M, N, K, _r(a), _r(b), _r(c), FAKE + 8, need, None) == s2r.S2R_ERR_ALIGN
+
+
+def test_a_weight_gradients_workspace_is_checked(s2r):
+    L = s2r.lib()
+    need = s2r.s2r_q8_wgrad_workspace_bytes(8192, 1024, 256)
+    assert need > 0
+    dy, x = _m(s2r, ld=1024), _q(s2r, lds=8192)
+    call = lambda ws, n: L.s2r_q8_wgrad(8192, 1024, 256, _r(dy), None, _r(x), FAKE, 256, 0, ws, n, None)
+    assert call(FAKE, need - 1) == s2r.S2R_ERR_WORKSPACE
+    assert call(FAKE + 8, need) == s2r.S2R_ERR_ALIGN
