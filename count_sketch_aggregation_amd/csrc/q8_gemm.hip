@@ -39,7 +39,6 @@ __device__ inline void each(F&& f) {
 }
 
 // ---- fragments ----------------------------------------------------------------------------
-// `at` is the byte of `sa` that holds this fragment's scale.
 __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
   i32x8 v;
 #pragma unroll
@@ -65,6 +64,7 @@ __device__ inline void clear_from(i32x8& v, int left) {  // `left` bytes stay
   }
 }
 
+// `at` is the byte of `sa` that holds this fragment's scale.
 template <int FA, int FB>
 __device__ inline f32x16 mma32(const i32x8& b, const i32x8& a, const f32x16& c, uint32_t sb,
                                uint32_t sa, int at) {
@@ -406,7 +406,6 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
   drain_and_sync();
 }
 
-// ---- few rows: fragments of 16 rows --------------------------------------------------------
 // ---- few rows -----------------------------------------------------------------------------
 // Up to 16 FM rows of A: the rows of B are read once, straight into registers, and bound the
 // call.  A workgroup takes 16 of them and cuts the sum among its waves, block by block in
@@ -422,13 +421,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
                                                             uint32_t M, uint32_t N, uint32_t K) {
   __shared__ f32x4 part[WAVES][FM][64];
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
-  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * FM);
+  const uint32_t n0 = blockIdx.x * 16;
   const uint32_t n = min(n0 + r, N - 1);
   const uint8_t* rows_a[FM];
   uint32_t ms[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    ms[i] = min(m0 + 16 * i + r, M - 1);
+    ms[i] = min(16 * i + r, M - 1);
     rows_a[i] = a.q + (uint64_t)ms[i] * a.ld;
   }
   const uint8_t* row_b = b.q + (uint64_t)n * b.ld;
@@ -469,7 +468,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
     f32x4 v = part[0][e / 64][e % 64];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += part[w][e / 64][e % 64];
-    const uint32_t m = m0 + e / 64 * 16 + e % 16, at = n0 + e % 64 / 16 * 4;
+    const uint32_t m = e / 64 * 16 + e % 16, at = n0 + e % 64 / 16 * 4;
     if (m < M) store4(c, m, at, N, v);
   }
 }
@@ -526,8 +525,8 @@ GemmPlan gemm_plan(uint64_t M, uint64_t N, uint64_t K, bool wide) {
 }
 
 // More than 32 rows of A are read so often that a large B is better off in tiles, if their sum can
-// be cut: 64 x 8192 x 4096 17.7 us in tiles, 24.6 without; 64 x 4096 x 4096 13.6 either way; 64 x 2000
-// x 2000 10.4 and 6.6.
+// be cut: 64 x 8192 x 4096 16.1 us in tiles (13.8 s2r_q8_gemm_fast), 23.7 without, 40 rows 15.3 (12.6)
+// and 19.9; 64 x 4096 x 4096 (13.6) and 12.8; 64 x 2000 x 2000 (10.4) and 6.4.
 bool few_rows(uint64_t M, uint64_t N, uint64_t K, bool workspace) {
   return M <= 32 || (M <= 64 && (N * K < 1ull << 25 || !workspace));
 }

@@ -36,17 +36,18 @@
  *   - Matrices are row-major with unit stride along a row.  q, scale and every s2r_mat are
  *     described by the host structs below, copied at call time.
  *   - Alignment: q and data 16 bytes, ld a multiple of 16 bytes (ld % 16 for codes, % 8 for
- *     16-bit and % 4 for fp32 elements); scale 4 bytes and lds % 4 == 0.  The elements after
- *     a row's last column up to a multiple of 16 bytes exist, are never written, and may hold
- *     anything; nothing beyond them is touched.  So a matrix may be a range of columns of a
- *     wider one (of 8-bit ones from a multiple of 128 on, with the scales of its blocks), and two
- *     products that add up, as dX = dG Wg + dU Wu, are one of matrices side by side.
+ *     16-bit and % 4 for fp32 elements); scale 4 bytes and lds % 4 == 0, each scale row whole.
+ *     The elements after a row's last column up to a multiple of 16 bytes exist, are never
+ *     written, and may hold anything; nothing beyond them is touched.  So a matrix may be a
+ *     range of columns of a wider one (of 8-bit ones from a multiple of 128 on, with the scales
+ *     of its blocks), and two products that add up, as dX = dG Wg + dU Wu, are one of matrices
+ *     side by side.
  *   - Sizes: rows and columns below 2^28; ld of at most 2^22 elements.  A size of 0 is a call
  *     that writes nothing, but an empty sum is a sum: K == 0 in s2r_q8_gemm writes zeros, and
  *     M == 0 in s2r_q8_wgrad without `accumulate` too.
  *   - No output may overlap an input or another output.
- *   - Sums are fp32 in an order fixed by the sizes and the workspace's size: the same call
- *     gives the same bits on every run.
+ *   - Sums are fp32 in an order fixed by the sizes and by whether there is a workspace: the
+ *     same call gives the same bits on every run.
  *   - Errors: S2R_ERR_NULL, S2R_ERR_DIM (sizes, ld or lds too small or too large, an unknown
  *     dtype, format or act), S2R_ERR_ALIGN, S2R_ERR_WORKSPACE, S2R_ERR_HIP.
  */
@@ -102,7 +103,7 @@ size_t s2r_q8_gemm_workspace_bytes(uint64_t M, uint64_t N, uint64_t K);
 
 /* c[m][n] = sum over k < K of value(a[m][k]) * value(b[n][k]).
  * a [M][K] row blocks, b [N][K] square blocks, c [M][N] of any s2r_dtype.  Every product is
- * exact and every addition fp32; c is rounded once.
+ * exact as far as fp32 reaches and every addition fp32; c is rounded once.
  * Layer output: a = X, b = W [N][K].  Input gradient: a = dY, b = the
  * transposed copy of s2r_q8_weight.  Any M from one token up.
  * workspace may be NULL (or ws_bytes 0): the sum is then never cut.  Otherwise it holds at
