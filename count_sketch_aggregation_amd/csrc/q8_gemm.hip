@@ -15,10 +15,11 @@
 // chooses.
 //
 // Measured on MI355X, 16384 x 8192 x 4096 e4m3 to bf16, many passes in turn over three sets of inputs:
-// s2r_q8_gemm 757 us, 1.45 PFLOP/s (a library's product of bf16 matrices 720), s2r_q8_gemm_fast 427 us,
-// 2.57 PFLOP/s (a library's with one scale for a whole matrix 391).  There a block of the sum of a
-// 256 x 256 tile takes 2400 to 2700 cycles where its matrix instructions alone take 2048; zeros run
-// 18% faster than random codes, so the rest is mostly power.
+// s2r_q8_gemm 763 us, 1.44 PFLOP/s (a library's product of bf16 matrices 704), its matrix cores busy for
+// 77% of the cycles; s2r_q8_gemm_fast 429 us, 2.56 PFLOP/s (a library's with one scale for a whole
+// matrix 367), 68%.  There a block of the sum of a 256 x 256 tile takes 2400 to 2700 cycles where its
+// matrix instructions alone take 2048; zeros run 18% faster than random codes, so the rest is
+// mostly power.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

@@ -9,10 +9,11 @@
 //   GELU_TANH  s = 1 / (1 + e^(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3), which is
 //              (1 + tanh z) / 2:             act = g s,  act' = s + g s (1 - s) 2 z'
 // Element-wise apart from the blocks' largest magnitudes: one read and one write of
-// everything, bound by HBM.  Measured on MI355X: gated SiLU of 8192 x 8192 bf16 with its three 8-bit
-// results 87 us (5.4 TB/s), its gradient 83 us (4.9); with the library's exponential and division the
-// gradient took 97 and was bound by arithmetic.  GELU takes 96 and 100; with the library's error
-// function, whose 1 + erf has no digits left far below zero, it took 89 and 108.
+// everything, bound by HBM and, where arithmetic comes close, by both.  Measured on MI355X: gated SiLU of
+// 8192 x 8192 bf16 with its three 8-bit results 88 us (5.3 TB/s), its gradient 86 us (4.7); with the
+// library's exponential and division the gradient took 97.  GELU_TANH takes 90 and 93, GELU 96 and
+// 100, bound by arithmetic (98% and 95% of the vector instructions that the cycles hold); with the
+// library's error function, whose 1 + erf has no digits left far below zero, GELU took 89 and 108.
 #include "q8_device.hpp"
 #include "q8_launch.hpp"
 
