@@ -23,11 +23,11 @@ constexpr int kGluThreads = 256;
 constexpr int kGluRows = kGluThreads / 8;
 constexpr int kGluBlocks = 2;  // blocks of 128 columns per workgroup: two or three streams each
 
-// e^x within two units in the last place at every x: x log2(e) is cut into a whole number and a
+// e^x within two units in the last place for |x| up to 200: x log2(e) is cut into a whole number and a
 // rest that keeps its low bits, and the hardware's 2^x (one unit) takes the rest.  Without that the
 // argument's rounding alone costs |x| half units, and a result next to a border of the 8-bit
-// grid falls to the other side that much more often.  Beyond +-200 it is infinite or zero; a NaN gets
-// lost, but what exp_of's callers multiply it with is the same NaN.
+// grid falls to the other side that much more often.  Beyond that e^x is infinite or zero, as it is at
+// 200; a NaN gets lost there, but what exp_of's callers multiply it with is the same NaN.
 __device__ inline float exp_within_200(float x) {
   const float n = __builtin_rintf(x * 1.44269504088896f);
   float r = __builtin_fmaf(x, 1.44269504088896f, -n);

@@ -8,7 +8,9 @@ row of the gradient matrix; block-wise Top-K with error feedback makes the rows 
 encode, reduce and decode aggregate them (include/s2r.h).  The target is a fixed layer of the
 same shape.
 
-    python examples/q8_training.py [--steps 40] [--workers 4] [--tokens 512]
+    python examples/q8_training.py [--steps 40] [--workers 4] [--tokens 512] [--fast]
+
+--fast takes the products at the 8-bit matrix rate, which cuts them short (include/s2r_q8.h).
 """
 import argparse
 import os
@@ -33,7 +35,8 @@ class FeedForward:
     """The layer's fp32 weights, one after the other in `flat`, their 8-bit copies, and the
     buffers of one pass over `tokens` rows; width and hidden are multiples of 4."""
 
-    def __init__(self, tokens, width, hidden, dev="cuda"):
+    def __init__(self, tokens, width, hidden, dev="cuda", fast=False):
+        self.gemm = s2r.s2r_q8_gemm_fast if fast else s2r.s2r_q8_gemm
         self.M, self.D, self.F = tokens, width, hidden
         M, D, F = tokens, width, hidden
         self.n = 3 * D * F
@@ -68,10 +71,10 @@ class FeedForward:
     def forward(self, x):
         M, D, F = self.M, self.D, self.F
         s2r.s2r_q8_save(M, D, s2r.mat(x), self.x8)
-        s2r.s2r_q8_gemm(M, F, D, self.x8, self.wg8, s2r.mat(self.g), workspace=self.ws)
-        s2r.s2r_q8_gemm(M, F, D, self.x8, self.wu8, s2r.mat(self.u), workspace=self.ws)
+        self.gemm(M, F, D, self.x8, self.wg8, s2r.mat(self.g), workspace=self.ws)
+        self.gemm(M, F, D, self.x8, self.wu8, s2r.mat(self.u), workspace=self.ws)
         s2r.s2r_q8_glu(M, F, "silu", s2r.mat(self.g), s2r.mat(self.u), gq=self.g8, uq=self.u8, yq=self.y8)
-        s2r.s2r_q8_gemm(M, D, F, self.y8, self.wd8, s2r.mat(self.out), workspace=self.ws)
+        self.gemm(M, D, F, self.y8, self.wd8, s2r.mat(self.out), workspace=self.ws)
         return self.out
 
     def backward(self, out_grad, row):
@@ -80,7 +83,7 @@ class FeedForward:
         dwg, dwu, dwd = self.views(row)
         s2r.s2r_q8_wgrad(M, D, F, s2r.mat(out_grad), self.y8, dwd, F, workspace=self.ws)
         s2r.s2r_q8_save(M, D, s2r.mat(out_grad), self.out_grad8)
-        s2r.s2r_q8_gemm(M, F, D, self.out_grad8, self.wd8t, s2r.mat(self.dy), workspace=self.ws)
+        self.gemm(M, F, D, self.out_grad8, self.wd8t, s2r.mat(self.dy), workspace=self.ws)
         s2r.s2r_q8_glu_grad(M, F, "silu", self.g8, self.u8, s2r.mat(self.dy), dgq=self.dg8, duq=self.du8)
         s2r.s2r_q8_wgrad(M, F, D, self.dg8, self.x8, dwg, D, workspace=self.ws)
         s2r.s2r_q8_wgrad(M, F, D, self.du8, self.x8, dwu, D, workspace=self.ws)
@@ -117,10 +120,11 @@ class Aggregation:
         return self.sum
 
 
-def train(steps=40, workers=4, tokens=512, width=256, hidden=512, lr=40.0, dev="cuda", log=print):
+def train(steps=40, workers=4, tokens=512, width=256, hidden=512, lr=40.0, dev="cuda", log=print,
+          fast=False):
     """The loss of every step."""
     torch.manual_seed(0)
-    layer, goal = FeedForward(tokens, width, hidden, dev), FeedForward(tokens, width, hidden, dev)
+    layer, goal = (FeedForward(tokens, width, hidden, dev, f) for f in (fast, False))
     goal.weights_to_8_bits()
     aggregate = Aggregation(workers, layer.n, dev=dev)
     x = [matrix(tokens, width, dev).normal_() for _ in range(workers)]
@@ -145,8 +149,9 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in [("steps", 40), ("workers", 4), ("tokens", 512)]:
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--fast", action="store_true")
     a = ap.parse_args()
-    train(a.steps, a.workers, a.tokens)
+    train(a.steps, a.workers, a.tokens, fast=a.fast)
 
 
 if __name__ == "__main__":

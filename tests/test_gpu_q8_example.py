@@ -70,3 +70,10 @@ def test_readme_examples():
     assert bool(((y - x @ w.t()).abs() <= 2 * (2 * 2.0 ** -4 + 2.0 ** -8) * mass).all())
     want = x.sum(0).expand_as(w)
     assert bool(((dw - want).abs() <= 2 * 2.0 ** -4 * x.abs().sum(0)).all())
+
+
+def test_training_learns_with_fast_products(example):
+    gp.say("q8 example training, fast")
+    losses = example.train(steps=30, log=None, fast=True)
+    assert all(l == l for l in losses)
+    assert losses[-1] < 0.5 * losses[0]
