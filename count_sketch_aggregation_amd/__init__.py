@@ -80,6 +80,19 @@ class s2r_q8_mat(ctypes.Structure):
                 ("lds", ctypes.c_uint64), ("format", ctypes.c_uint32)]
 
 
+class s2r_q4_mat(ctypes.Structure):
+    """Mirror of ``s2r_q4_mat`` in include/s2r_q4.h; made from tensors by q4_mat() or alloc_q4()."""
+
+    _fields_ = [("q", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("scale", ctypes.c_void_p),
+                ("lds", ctypes.c_uint64)]
+
+
+class s2r_experts(ctypes.Structure):
+    """Mirror of ``s2r_experts`` in include/s2r_moe.h; made from tensors by experts()."""
+
+    _fields_ = [("first", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("experts", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -150,6 +163,26 @@ def lib() -> ctypes.CDLL:
         L.s2r_q8_glu_grad.argtypes = [u64, u64, ctypes.c_int, pq, pq, pm, pm, pm, pq, pq, vp]
         for f in (L.s2r_q8_save, L.s2r_q8_load, L.s2r_q8_weight, L.s2r_q8_gemm, L.s2r_q8_gemm_fast,
                   L.s2r_q8_wgrad, L.s2r_q8_glu, L.s2r_q8_glu_grad):
+            f.restype = st
+        pe, p4, ci = P(s2r_experts), P(s2r_q4_mat), ctypes.c_int
+        L.s2r_moe_rows.argtypes = [u64, u32, u32]
+        L.s2r_moe_rows.restype = u64
+        L.s2r_moe_route_workspace_bytes.argtypes = [u64, u32, u32]
+        L.s2r_moe_route_workspace_bytes.restype = sz
+        L.s2r_moe_route.argtypes = [u64, u32, u32, vp, vp, vp, vp, vp, sz, vp]
+        L.s2r_moe_gather.argtypes = [u64, u32, u64, pm, vp, u64, pm, pq, vp]
+        L.s2r_moe_combine.argtypes = [u64, u32, u64, pm, u64, vp, vp, pm, vp]
+        L.s2r_moe_combine_grad.argtypes = [u64, u32, u64, pm, vp, u64, vp, pm, pm, pq, vp, vp]
+        L.s2r_q8_gemm_experts.argtypes = [u64, u64, u64, pe, pq, pq, u64, u64, pm, vp]
+        L.s2r_q8_wgrad_experts.argtypes = [u64, u64, u64, pe, pm, pq, pq, vp, u64, u64, ci, vp]
+        L.s2r_q4_save.argtypes = [u64, u64, pm, p4, p4, vp]
+        L.s2r_q4_load.argtypes = [u64, u64, p4, pm, vp]
+        L.s2r_q4_gemm_workspace_bytes.argtypes = [u64, u64, u64]
+        L.s2r_q4_gemm_workspace_bytes.restype = sz
+        L.s2r_q4_gemm.argtypes = [u64, u64, u64, p4, p4, pm, vp, sz, vp]
+        for f in (L.s2r_moe_route, L.s2r_moe_gather, L.s2r_moe_combine, L.s2r_moe_combine_grad,
+                  L.s2r_q8_gemm_experts, L.s2r_q8_wgrad_experts, L.s2r_q4_save, L.s2r_q4_load,
+                  L.s2r_q4_gemm):
             f.restype = st
         L.s2r_status_string.argtypes = [st]
         L.s2r_status_string.restype = ctypes.c_char_p
@@ -419,6 +452,146 @@ def s2r_q8_glu_grad(M: int, F: int, act, gq: s2r_q8_mat, uq: s2r_q8_mat | None, 
                                  _ref(dgq), _ref(duq), _stream(stream)), "s2r_q8_glu_grad")
 
 
+# ---------------------------------------------------------------------------------------
+# layers of experts (include/s2r_moe.h)
+
+
+def _ints(t, shape, where):
+    """Device pointer of a dense int32 tensor of `shape` (None and addresses pass through)."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype not in (torch.int32, torch.uint32) or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise S2RError(S2R_ERR_DIM, where)
+    return t.data_ptr()
+
+
+def _floats(t, shape, where):
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise S2RError(S2R_ERR_DIM, where)
+    return t.data_ptr()
+
+
+def experts(first, rows) -> s2r_experts:
+    """Descriptor of the experts' rows, two int32 tensors [E]; keeps them alive."""
+    E = rows.numel()
+    e = s2r_experts(_ints(first, (E,), "experts"), _ints(rows, (E,), "experts"), E)
+    e.tensors = first, rows
+    return e
+
+
+def s2r_moe_rows(T: int, K: int, E: int) -> int:
+    """Rows that always hold the K choices of T tokens among E experts."""
+    return int(lib().s2r_moe_rows(T, K, E))
+
+
+def s2r_moe_route_workspace_bytes(T: int, K: int, E: int) -> int:
+    return int(lib().s2r_moe_route_workspace_bytes(T, K, E))
+
+
+def s2r_moe_route(T: int, K: int, E: int, expert, first, rows, place, workspace=None,
+                  ws_bytes: int | None = None, stream=None) -> None:
+    """expert [T][K] -> first [E] and rows [E] of every expert, place [T][K] of every choice
+    (int32, dense; -1: none)."""
+    w = "s2r_moe_route"
+    ws, nb = _ws(workspace, ws_bytes)
+    _check(lib().s2r_moe_route(T, K, E, _ints(expert, (T, K), w), _ints(first, (E,), w), _ints(rows, (E,), w),
+                               _ints(place, (T, K), w), ws, nb, _stream(stream)), w)
+
+
+def s2r_moe_gather(T: int, K: int, D: int, x: s2r_mat, place, R: int, out: s2r_mat | None = None,
+                   outq: s2r_q8_mat | None = None, stream=None) -> None:
+    """Every token of x [T][D] to its choices' rows of out and, in 8 bits, of outq [R][D]."""
+    w = "s2r_moe_gather"
+    _check(lib().s2r_moe_gather(T, K, D, _ref(x), _ints(place, (T, K), w), R, _ref(out), _ref(outq),
+                                _stream(stream)), w)
+
+
+def s2r_moe_combine(T: int, K: int, D: int, rows: s2r_mat, R: int, place, weight, y: s2r_mat,
+                    stream=None) -> None:
+    """y [T][D] = the sum of every token's rows of rows [R][D], with weight [T][K] (None: ones)."""
+    w = "s2r_moe_combine"
+    _check(lib().s2r_moe_combine(T, K, D, _ref(rows), R, _ints(place, (T, K), w), _floats(weight, (T, K), w),
+                                 _ref(y), _stream(stream)), w)
+
+
+def s2r_moe_combine_grad(T: int, K: int, D: int, dy: s2r_mat, place, R: int, weight=None,
+                         rows: s2r_mat | None = None, drows: s2r_mat | None = None,
+                         drowsq: s2r_q8_mat | None = None, dweight=None, stream=None) -> None:
+    """The gradients of s2r_moe_combine's rows (drows, and drowsq in 8 bits) and weights (dweight
+    [T][K], from rows)."""
+    w = "s2r_moe_combine_grad"
+    _check(lib().s2r_moe_combine_grad(T, K, D, _ref(dy), _ints(place, (T, K), w), R, _floats(weight, (T, K), w),
+                                      _ref(rows), _ref(drows), _ref(drowsq), _floats(dweight, (T, K), w),
+                                      _stream(stream)), w)
+
+
+def s2r_q8_gemm_experts(M: int, N: int, K: int, e: s2r_experts, a: s2r_q8_mat, b: s2r_q8_mat, b_step: int,
+                        b_scale_step: int, c: s2r_mat, stream=None) -> None:
+    """c = a b_e^T for the rows of every expert; b is expert 0's [N][K], expert e's is e * b_step and
+    e * b_scale_step bytes further on."""
+    _check(lib().s2r_q8_gemm_experts(M, N, K, _ref(e), _ref(a), _ref(b), b_step, b_scale_step, _ref(c),
+                                     _stream(stream)), "s2r_q8_gemm_experts")
+
+
+def s2r_q8_wgrad_experts(M: int, N: int, K: int, e: s2r_experts, dy, x: s2r_q8_mat, dw, lddw: int, dw_step: int,
+                         accumulate: bool = False, stream=None) -> None:
+    """dw + e * dw_step [N][lddw] (+)= dy^T x over the rows of every expert e, as s2r_q8_wgrad."""
+    wide = isinstance(dy, s2r_mat)
+    _check(lib().s2r_q8_wgrad_experts(M, N, K, _ref(e), _ref(dy) if wide else None, None if wide else _ref(dy),
+                                      _ref(x), _ptr(dw), lddw, dw_step, 1 if accumulate else 0,
+                                      _stream(stream)), "s2r_q8_wgrad_experts")
+
+
+# ---------------------------------------------------------------------------------------
+# matrices in 4 bits (include/s2r_q4.h)
+
+
+def q4_mat(q, scale) -> s2r_q4_mat:
+    """Descriptor of a 4-bit matrix: q [rows][ld] bytes of two codes and scale [rows][lds] bytes; keeps
+    the tensors alive."""
+    for t in (q, scale):
+        if t.dim() != 2 or t.element_size() != 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise S2RError(S2R_ERR_DIM, "q4_mat")
+    ld, lds = (max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0) for t in (q, scale))
+    m = s2r_q4_mat(q.data_ptr(), ld, scale.data_ptr(), lds)
+    m.codes, m.scales = q, scale
+    return m
+
+
+def alloc_q4(rows: int, cols: int, device="cuda") -> s2r_q4_mat:
+    """A 4-bit matrix on new tensors (.codes, .scales), padded as the calls need it."""
+    import torch
+    up = lambda n, m: -(-n // m) * m
+    return q4_mat(torch.empty((rows, up(max(cols, 1), 32) // 2), dtype=torch.uint8, device=device),
+                  torch.empty((rows, up(max(cols, 1), 256) // 32), dtype=torch.uint8, device=device))
+
+
+def s2r_q4_save(R: int, C: int, x: s2r_mat, out: s2r_q4_mat | None = None, out_t: s2r_q4_mat | None = None,
+                stream=None) -> None:
+    """x [R][C] to 4 bits, and its transpose [C][R], one scale per 32 elements of their rows."""
+    _check(lib().s2r_q4_save(R, C, _ref(x), _ref(out), _ref(out_t), _stream(stream)), "s2r_q4_save")
+
+
+def s2r_q4_load(R: int, C: int, q: s2r_q4_mat, x: s2r_mat, stream=None) -> None:
+    """The stored values of q [R][C] into x."""
+    _check(lib().s2r_q4_load(R, C, _ref(q), _ref(x), _stream(stream)), "s2r_q4_load")
+
+
+def s2r_q4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().s2r_q4_gemm_workspace_bytes(M, N, K))
+
+
+def s2r_q4_gemm(M: int, N: int, K: int, a: s2r_q4_mat, b: s2r_q4_mat, c: s2r_mat, workspace=None,
+                ws_bytes: int | None = None, stream=None) -> None:
+    """c [M][N] = a [M][K] b [N][K]^T."""
+    ws, nb = _ws(workspace, ws_bytes)
+    _check(lib().s2r_q4_gemm(M, N, K, _ref(a), _ref(b), _ref(c), ws, nb, _stream(stream)), "s2r_q4_gemm")
+
+
 TRACE_MAX = 64
 
 
@@ -488,6 +661,9 @@ __all__ = [
     "s2r_mat", "s2r_q8_mat", "mat", "q8_mat", "alloc_q8", "s2r_q8_save", "s2r_q8_load",
     "s2r_q8_weight", "s2r_q8_gemm_workspace_bytes", "s2r_q8_gemm", "s2r_q8_gemm_fast",
     "s2r_q8_wgrad_workspace_bytes", "s2r_q8_wgrad", "s2r_q8_glu", "s2r_q8_glu_grad",
+    "s2r_experts", "experts", "s2r_moe_rows", "s2r_moe_route_workspace_bytes", "s2r_moe_route", "s2r_moe_gather",
+    "s2r_moe_combine", "s2r_moe_combine_grad", "s2r_q8_gemm_experts", "s2r_q8_wgrad_experts",
+    "s2r_q4_mat", "q4_mat", "alloc_q4", "s2r_q4_save", "s2r_q4_load", "s2r_q4_gemm_workspace_bytes", "s2r_q4_gemm",
     "s2r_trace", "s2r_diag_trace_attach",
     "alloc_encode_buffers", "status_string", "lib",
 ]

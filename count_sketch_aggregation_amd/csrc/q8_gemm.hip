@@ -24,6 +24,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "moe_launch.hpp"
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
@@ -474,6 +475,70 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few(s2r_q8_mat a, s2r_q8
   }
 }
 
+// ---- few rows of an expert ------------------------------------------------------------------
+// The same for the rows of experts, 16 at a time: a workgroup takes 16 columns of the experts with
+// rows, gridDim.y apart in their order.  first and rows are cut at M.
+struct ExpertRows {
+  uint32_t expert, first, end;
+};
+// The `nth` expert with rows, found by the lanes of every wave; expert ~0 where there are fewer.
+__device__ inline ExpertRows nth_expert(const s2r_experts& e, uint32_t M, uint32_t nth) {
+  const uint32_t lane = threadIdx.x % 64;
+  for (uint32_t base = 0; base < e.experts; base += 64) {
+    const bool there = base + lane < e.experts;
+    const uint32_t first = there ? min(e.first[base + lane], M) : 0;
+    const uint32_t rows = there ? min(e.rows[base + lane], M - first) : 0;
+    const uint64_t some = __ballot(rows > 0);
+    const uint32_t n = (uint32_t)__popcll(some);
+    if (nth < n) {
+      const bool is = rows > 0 && (uint32_t)__popcll(some & ((1ull << lane) - 1)) == nth;
+      const uint32_t at = (uint32_t)__builtin_ctzll(__ballot(is));
+      const uint32_t f = __builtin_amdgcn_readlane(first, at);
+      return {base + at, f, f + (uint32_t)__builtin_amdgcn_readlane(rows, at)};
+    }
+    nth -= n;
+  }
+  return {~0u, 0, 0};
+}
+
+template <int FA, int FB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few_experts(s2r_q8_mat a, s2r_q8_mat b, ExpertSteps steps,
+                                                                    s2r_mat c, s2r_experts experts, uint32_t M,
+                                                                    uint32_t N, uint32_t K) {
+  __shared__ f32x4 part[WAVES][64];
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+  const uint32_t n0 = blockIdx.x * 16, n = min(n0 + r, N - 1);
+  const uint32_t blocks = (K + kQ8Block - 1) / kQ8Block;
+  for (uint32_t nth = blockIdx.y;; nth += gridDim.y) {
+    const ExpertRows x = nth_expert(experts, M, nth);
+    if (x.expert == ~0u) return;
+    const uint8_t* row_b = b.q + x.expert * steps.step + (uint64_t)n * b.ld;
+    const uint8_t* scale_b = b.scale + x.expert * steps.scale_step + n0 / kQ8Block;
+    for (uint32_t m0 = x.first; m0 < x.end; m0 += 16) {
+      const uint32_t m = min(m0 + r, x.end - 1);
+      const uint8_t* row_a = a.q + (uint64_t)m * a.ld;
+      f32x4 acc = {};
+      for (uint32_t s = wave; s < blocks; s += WAVES) {
+        const uint32_t k = s * kQ8Block + 16 * g;
+        const i32x8 fb = load_frag(row_b, k, K), fa = load_frag(row_a, k, K);
+        const uint32_t sb = scale_b[(uint64_t)s * b.lds], sa = a.scale[(uint64_t)s * a.lds + m];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<FB>(fb, p, sb), widen8<FA>(fa, p, sa), acc, 0, 0, 0);
+      }
+      part[wave][lane] = acc;
+      __syncthreads();
+      if (wave == 0) {
+        f32x4 v = part[0][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v += part[w][lane];
+        if (m0 + r < x.end && n0 + 4 * g < N) store4(c, m0 + r, n0 + 4 * g, N, v);
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // The parts of a sum, added in their order.
 constexpr int kSumThreads = 256;
 __global__ __launch_bounds__(kSumThreads) void k_q8_gemm_sum(const float* __restrict__ part,
@@ -612,6 +677,26 @@ hipError_t launch_q8_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q8_mat& 
     if (b.format == S2R_E4M3) go_gemm<S2R_E5M2, S2R_E4M3>(M, N, K, a, b, c, fast, workspace, s);
     else go_gemm<S2R_E5M2, S2R_E5M2>(M, N, K, a, b, c, fast, workspace, s);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_gemm_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e,
+                                  const s2r_q8_mat& a, const s2r_q8_mat& b, ExpertSteps steps,
+                                  const s2r_mat& c, hipStream_t s) {
+  // experts with rows are at least 4 rows apart
+  const dim3 grid((uint32_t)((N + 15) / 16), (uint32_t)std::min<uint64_t>(e.experts, (M + 3) / 4));
+  trace_mark(s, "k_q8_gemm_few_experts");
+#define S2R_FEW(FA, FB)                                                                                  \
+  hipLaunchKernelGGL((k_q8_gemm_few_experts<FA, FB, 8>), grid, dim3(512), 0, s, a, b, steps, c, e, (uint32_t)M, \
+                     (uint32_t)N, (uint32_t)K)
+  if (a.format == S2R_E4M3) {
+    if (b.format == S2R_E4M3) S2R_FEW(S2R_E4M3, S2R_E4M3);
+    else S2R_FEW(S2R_E4M3, S2R_E5M2);
+  } else {
+    if (b.format == S2R_E4M3) S2R_FEW(S2R_E5M2, S2R_E4M3);
+    else S2R_FEW(S2R_E5M2, S2R_E5M2);
+  }
+#undef S2R_FEW
   return hipGetLastError();
 }
 

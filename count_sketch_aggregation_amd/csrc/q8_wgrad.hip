@@ -11,6 +11,7 @@
 // faster than random values.
 #include <algorithm>
 
+#include "moe_launch.hpp"
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
@@ -148,11 +149,12 @@ struct Feed {
 // read while the step before is multiplied, so a block's LDS is free before its last step:
 // there the block after the next begins to arrive.  Codes come to registers a block before, and
 // are decoded all along the next one's steps.
-template <int KY, int FX, int WM, int WN, int FM, int FN>
+// With EXPERTS the parts are the experts, each with its own rows and its own dw.
+template <int KY, int FX, int WM, int WN, int FM, int FN, bool EXPERTS>
 __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgrad(
     s2r_mat dy16, s2r_q8_mat dy8, s2r_q8_mat xq, float* dw, uint64_t lddw, uint64_t part_floats,
     uint32_t M, uint32_t N, uint32_t K, bool accumulate, uint32_t n_tiles, uint32_t k_tiles,
-    uint32_t part_rows) {
+    uint32_t part_rows, s2r_experts experts) {
   constexpr int kWaves = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
   using Y = Feed<KY, TM, kWaves>;
   using X = Feed<FX, TN, kWaves>;
@@ -163,7 +165,12 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgra
   const TileAt t = tile_at(blockIdx.x, n_tiles, k_tiles, gridDim.x);
   const uint32_t n0 = t.row * TM, k0 = t.col * TN;
   const uint32_t wm = wave / WN * (32 * FM), wn = wave % WN * (32 * FN);
-  const uint32_t m0 = t.part * part_rows, m1 = min(m0 + part_rows, M);
+  uint32_t m0 = t.part * part_rows, m1 = min(m0 + part_rows, M);
+  if (EXPERTS) {
+    m0 = min(experts.first[t.part], M);
+    m1 = m0 + min(experts.rows[t.part], M - m0);
+    if (m0 == m1 && accumulate) return;
+  }
 
   struct Frags {
     bf16x8 y[FM], x[FN];
@@ -377,17 +384,41 @@ void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8
   const bool add = accumulate && !cut;
   trace_mark(s, "k_q8_wgrad");
   if (p.side == 256)
-    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 4, 4, 2>), dim3(grid), dim3(512), 0, s, d, q, x, to, ld,
-                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows);
+    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 4, 4, 2, false>), dim3(grid), dim3(512), 0, s, d, q, x, to, ld,
+                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows, s2r_experts{});
   else
-    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
-                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows);
+    hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2, false>), dim3(grid), dim3(256), 0, s, d, q, x, to, ld,
+                       p.part_floats, (uint32_t)M, (uint32_t)N, (uint32_t)K, add, p.nt, p.kt, rows, s2r_experts{});
   if (!cut) return;
   trace_mark(s, "k_q8_wgrad_sum");
   const uint64_t quads = N * ((K + 3) / 4);
   hipLaunchKernelGGL(k_q8_wgrad_sum, dim3((uint32_t)((quads + kSumThreads - 1) / kSumThreads)),
                      dim3(kSumThreads), 0, s, workspace, p.part_floats, p.cut.parts, dw, lddw,
                      (uint32_t)N, (uint32_t)K, accumulate);
+}
+
+// Tiles of 256 where they fill the GPU, else of 128.  An expert's sum is not cut: there are as many sums
+// as experts.
+template <int KY, int FX>
+void go_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, const s2r_mat& d,
+                      const s2r_q8_mat& q, const s2r_q8_mat& x, float* dw, uint64_t lddw, uint64_t dw_step,
+                      bool accumulate, hipStream_t s) {
+  auto tiles = [&](uint64_t n, uint64_t side) { return (uint32_t)((n + side - 1) / side); };
+  const bool large = (uint64_t)tiles(N, 256) * tiles(K, 256) * e.experts >= kTileCus;
+  const uint32_t side = large ? 256 : 128, nt = tiles(N, side), kt = tiles(K, side);
+  // a launch holds below 2^32 threads
+  const uint32_t most = std::max<uint64_t>(1, ((1ull << 32) - 1) / ((uint64_t)nt * kt * 512));
+  trace_mark(s, "k_q8_wgrad_experts");
+  for (uint32_t i = 0; i < e.experts; i += most) {
+    const s2r_experts of = {e.first + i, e.rows + i, std::min(e.experts - i, most)};
+    const dim3 grid(nt * kt * of.experts);
+    if (large)
+      hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 4, 4, 2, true>), grid, dim3(512), 0, s, d, q, x, dw + i * dw_step,
+                         lddw, dw_step, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, 0, of);
+    else
+      hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2, true>), grid, dim3(256), 0, s, d, q, x, dw + i * dw_step,
+                         lddw, dw_step, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, 0, of);
+  }
 }
 
 }  // namespace
@@ -397,6 +428,21 @@ size_t q8_wgrad_workspace(uint64_t M, uint64_t N, uint64_t K) {
   return p.cut.parts > 1 ? p.cut.parts * p.part_floats * sizeof(float) : 0;
 }
 
+// S2R_WGRAD for the kinds of dy and x
+#define S2R_WGRAD_KINDS(dy16, dy8, x)                                        \
+  do {                                                                       \
+    const int ky = dy16 ? kBf16 : (int)dy8->format;                          \
+    if (x.format == S2R_E4M3) {                                              \
+      if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E4M3);                           \
+      else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E4M3);                \
+      else S2R_WGRAD(S2R_E5M2, S2R_E4M3);                                    \
+    } else {                                                                 \
+      if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E5M2);                           \
+      else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E5M2);                \
+      else S2R_WGRAD(S2R_E5M2, S2R_E5M2);                                    \
+    }                                                                        \
+  } while (0)
+
 hipError_t launch_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy16,
                            const s2r_q8_mat* dy8, const s2r_q8_mat& x, float* dw, uint64_t lddw,
                            bool accumulate, void* workspace, hipStream_t s) {
@@ -404,16 +450,19 @@ hipError_t launch_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy
   const s2r_q8_mat q = dy8 ? *dy8 : s2r_q8_mat{};
   float* const ws = static_cast<float*>(workspace);
 #define S2R_WGRAD(KY, FX) go_wgrad<KY, FX>(M, N, K, d, q, x, dw, lddw, accumulate, ws, s)
-  const int ky = dy16 ? kBf16 : (int)dy8->format;
-  if (x.format == S2R_E4M3) {
-    if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E4M3);
-    else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E4M3);
-    else S2R_WGRAD(S2R_E5M2, S2R_E4M3);
-  } else {
-    if (ky == kBf16) S2R_WGRAD(kBf16, S2R_E5M2);
-    else if (ky == S2R_E4M3) S2R_WGRAD(S2R_E4M3, S2R_E5M2);
-    else S2R_WGRAD(S2R_E5M2, S2R_E5M2);
-  }
+  S2R_WGRAD_KINDS(dy16, dy8, x);
+#undef S2R_WGRAD
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e,
+                                   const s2r_mat* dy16, const s2r_q8_mat* dy8, const s2r_q8_mat& x,
+                                   float* dw, uint64_t lddw, uint64_t dw_step, bool accumulate,
+                                   hipStream_t s) {
+  const s2r_mat d = dy16 ? *dy16 : s2r_mat{};
+  const s2r_q8_mat q = dy8 ? *dy8 : s2r_q8_mat{};
+#define S2R_WGRAD(KY, FX) go_wgrad_experts<KY, FX>(M, N, K, e, d, q, x, dw, lddw, dw_step, accumulate, s)
+  S2R_WGRAD_KINDS(dy16, dy8, x);
 #undef S2R_WGRAD
   return hipGetLastError();
 }
