@@ -21,24 +21,12 @@
 // matrix instructions alone take 2048; zeros run 18% faster than random codes, so the rest is
 // mostly power.
 #include <algorithm>
-#include <type_traits>
-#include <utility>
 
 #include "moe_launch.hpp"
 #include "q8_launch.hpp"
 #include "q8_tile.hpp"
 
 namespace s2r {
-
-// f(first), ..., f(end - 1) with constants: the compiler gives up unrolling long bodies.
-template <int FIRST, class F, int... I>
-__device__ inline void each_of(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, FIRST + I>()), ...);
-}
-template <int FIRST, int END, class F>
-__device__ inline void each(F&& f) {
-  each_of<FIRST>(f, std::make_integer_sequence<int, END - FIRST>());
-}
 
 // ---- fragments ----------------------------------------------------------------------------
 __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
@@ -93,66 +81,6 @@ __device__ inline f32x16 mma32(const i32x8& b, const i32x8& a, const f32x16& c, 
 // scales of a lane's fragments are one load.
 // A workgroup stays for several tiles, and the blocks of all of them are one stream: the next
 // tile's first blocks arrive while the last ones of this are multiplied and its results leave.
-__host__ __device__ constexpr int lesser(int a, int b) { return a < b ? a : b; }
-__device__ inline uint32_t spread(uint32_t p) { return p / 2 % 4 | p / 16 % 2 << 2; }
-
-// ROWS x 64 results from LDS: rows m0, m0 + step, ..., columns n0 .. n0 + 63; lane l takes eight
-// columns of rows l / 8 + 8 k.  They leave through a view that ends with row M - 1; lanes
-// without eight columns aim beyond its end.
-template <int DT, int ROWS>
-__device__ inline void store_rows(const s2r_mat& c, const f32x4 (&v)[ROWS / 8][2], uint32_t m0, uint32_t step,
-                                  uint32_t M, uint32_t n0, uint32_t N) {
-  constexpr uint32_t size = elem_bytes<DT>(), kNowhere = 0xffff0000u;
-  const uint64_t first = (uint64_t)m0 * c.ld + n0, last = (uint64_t)(M - 1) * c.ld + N;
-  const auto view = rsrc_of((uint64_t)c.data + first * size, (last - first) * size);
-  const uint32_t lane = threadIdx.x % 64, n = lane % 8 * 8;
-  const uint32_t ld = step * (uint32_t)c.ld * size;
-  const uint32_t at = n0 + n < N ? lane / 8 * ld + n * size : kNowhere;
-#pragma unroll
-  for (uint32_t k = 0; k < ROWS / 8; ++k) {
-    const uint32_t to = n0 + n < N ? at + 8 * k * ld : kNowhere;
-    const f32x4 lo = v[k][0], hi = v[k][1];
-    if (DT == S2R_F32) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), view, to, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), view, to + 16, 0, 0);
-    } else {
-      __builtin_amdgcn_raw_buffer_store_b128(
-          u32x4{pack2<DT>(lo[0], lo[1]), pack2<DT>(lo[2], lo[3]), pack2<DT>(hi[0], hi[1]),
-                pack2<DT>(hi[2], hi[3])}, view, to, 0, 0);
-    }
-  }
-}
-
-template <int ROWS>
-__device__ inline void store_turned(const s2r_mat& c, const uint8_t* lds, uint32_t m0, uint32_t step,
-                                    uint32_t M, uint32_t n0, uint32_t N) {
-  if (m0 >= M || n0 >= N) return;
-  const uint32_t lane = threadIdx.x % 64, s = lane % 8 * 2;
-  if (n0 + 64 > N && N % 8 != 0) {  // a lane may have fewer than eight columns
-#pragma unroll 1
-    for (uint32_t row = lane / 8; row < ROWS; row += 8) {
-      const uint32_t m = m0 + step * row, n = n0 + lane % 8 * 8;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(lds + turned(row, s));
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(lds + turned(row, s + 1));
-      if (m < M && n < N) store8(c, m, n, N, lo, hi);
-    }
-    return;
-  }
-  f32x4 v[ROWS / 8][2];
-#pragma unroll
-  for (uint32_t k = 0; k < ROWS / 8; ++k) {
-    v[k][0] = *reinterpret_cast<const f32x4*>(lds + turned(lane / 8 + 8 * k, s));
-    v[k][1] = *reinterpret_cast<const f32x4*>(lds + turned(lane / 8 + 8 * k, s + 1));
-  }
-  if (c.dtype == S2R_BF16) {
-    store_rows<S2R_BF16, ROWS>(c, v, m0, step, M, n0, N);
-  } else if (c.dtype == S2R_F16) {
-    store_rows<S2R_F16, ROWS>(c, v, m0, step, M, n0, N);
-  } else {
-    store_rows<S2R_F32, ROWS>(c, v, m0, step, M, n0, N);
-  }
-}
-
 template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     s2r_q8_mat a, s2r_q8_mat b, s2r_mat c, uint64_t part_bytes, uint32_t M, uint32_t N, uint32_t K,
