@@ -218,8 +218,9 @@ __device__ inline void store_fragment(const f32x16& x, __amdgpu_buffer_rsrc_t vi
   }
 }
 
-// All FM x FN fragments of a wave.
-template <int FM, int FN>
+// All FM x FN fragments of a wave: lane r of fragment i has row m0 + 32 i + r, or with TURNS
+// m0 + FM r + i.
+template <int FM, int FN, bool TURNS = false>
 __device__ inline void store_wave(const s2r_mat& c, const f32x16 (&acc)[FM][FN], uint32_t m0, uint32_t M, uint32_t n0,
                                   uint32_t N) {
   const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
@@ -236,18 +237,19 @@ __device__ inline void store_wave(const s2r_mat& c, const f32x16 (&acc)[FM][FN],
       f32x16 x = acc[i][j];
       // stays where the matrix instruction left it until here: all of them would not fit beside each other
       asm volatile("" : "+a"(x));
+      const uint32_t row = TURNS ? FM * r + i : 32 * i + r;
       if (ragged || n + 32 > N) {
-        const uint32_t m = m0 + 32 * i + r;
+        const uint32_t m = m0 + row;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (m < M && n + 8 * q + 4 * g < N)
             store4(c, m, n + 8 * q + 4 * g, N, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
       } else if (c.dtype == S2R_BF16) {
-        store_fragment<S2R_BF16>(x, view, (32 * i + r) * ld + 64 * j + 16 * g);
+        store_fragment<S2R_BF16>(x, view, row * ld + 64 * j + 16 * g);
       } else if (c.dtype == S2R_F16) {
-        store_fragment<S2R_F16>(x, view, (32 * i + r) * ld + 64 * j + 16 * g);
+        store_fragment<S2R_F16>(x, view, row * ld + 64 * j + 16 * g);
       } else {
-        store_fragment<S2R_F32>(x, view, (32 * i + r) * ld + 128 * j + 16 * g);
+        store_fragment<S2R_F32>(x, view, row * ld + 128 * j + 16 * g);
       }
     }
 }
