@@ -149,7 +149,29 @@ struct Feed {
 // read while the step before is multiplied, so a block's LDS is free before its last step:
 // there the block after the next begins to arrive.  Codes come to registers a block before, and
 // are decoded all along the next one's steps.
-// With EXPERTS the parts are the experts, each with its own rows and its own dw.
+// With EXPERTS the parts are the experts, each with its own rows and its own dw.  Their sums differ in length, so an
+// expert's tiles go round all dies, and the longest sums begin first (for up to 64 experts; more are each a
+// small part of the whole).
+__device__ inline TileAt expert_tile_at(uint32_t b, uint32_t rows, uint32_t cols, const s2r_experts& e) {
+  const uint32_t tiles = rows * cols, lane = threadIdx.x % 64;
+  uint32_t part = b / tiles;
+  const uint32_t in = b - part * tiles;
+  if (e.experts <= 64) {
+    const uint32_t mine = lane < e.experts ? e.rows[lane] : 0;
+    uint32_t longer = 0;  // experts that begin before this lane's
+    for (uint32_t i = 0; i < e.experts; ++i) {
+      const uint32_t n = __builtin_amdgcn_readlane(mine, i);
+      longer += n > mine || (n == mine && i < lane);
+    }
+    part = (uint32_t)__builtin_ctzll(__ballot(lane < e.experts && longer == part));
+  }
+  TileAt t;
+  t.row = __builtin_amdgcn_readfirstlane(in % rows);
+  t.col = __builtin_amdgcn_readfirstlane(in / rows);
+  t.part = __builtin_amdgcn_readfirstlane(part);
+  return t;
+}
+
 template <int KY, int FX, int WM, int WN, int FM, int FN, bool EXPERTS>
 __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgrad(
     s2r_mat dy16, s2r_q8_mat dy8, s2r_q8_mat xq, float* dw, uint64_t lddw, uint64_t part_floats,
@@ -162,7 +184,8 @@ __global__ __launch_bounds__(64 * WM * WN, FM * FN == 16 ? 1 : 2) void k_q8_wgra
 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
-  const TileAt t = tile_at(blockIdx.x, n_tiles, k_tiles, gridDim.x);
+  const TileAt t = EXPERTS ? expert_tile_at(blockIdx.x, n_tiles, k_tiles, experts)
+                           : tile_at(blockIdx.x, n_tiles, k_tiles, gridDim.x);
   const uint32_t n0 = t.row * TM, k0 = t.col * TN;
   const uint32_t wm = wave / WN * (32 * FM), wn = wave % WN * (32 * FN);
   uint32_t m0 = t.part * part_rows, m1 = min(m0 + part_rows, M);
