@@ -212,7 +212,8 @@ def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without a Stream object around it, which costs as much as a short call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # ---------------------------------------------------------------------------------------
@@ -456,23 +457,23 @@ def s2r_q8_glu_grad(M: int, F: int, act, gq: s2r_q8_mat, uq: s2r_q8_mat | None, 
 # layers of experts (include/s2r_moe.h)
 
 
-def _ints(t, shape, where):
-    """Device pointer of a dense int32 tensor of `shape` (None and addresses pass through)."""
+def _dense(t, shape: tuple, dtypes: tuple, where: str):
+    """Device pointer of a dense tensor of `shape` (None and addresses pass through)."""
     if t is None or isinstance(t, int):
         return t
-    import torch
-    if t.dtype not in (torch.int32, torch.uint32) or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise S2RError(S2R_ERR_DIM, where)
     return t.data_ptr()
 
 
-def _floats(t, shape, where):
-    if t is None or isinstance(t, int):
-        return t
+def _ints(t, shape: tuple, where: str):
     import torch
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise S2RError(S2R_ERR_DIM, where)
-    return t.data_ptr()
+    return _dense(t, shape, (torch.int32, torch.uint32), where)
+
+
+def _floats(t, shape: tuple, where: str):
+    import torch
+    return _dense(t, shape, (torch.float32,), where)
 
 
 def experts(first, rows) -> s2r_experts:

@@ -190,10 +190,8 @@ struct Choices {
 };
 
 // ---- gather -------------------------------------------------------------------------------
-// A wave takes 4 KB of a token's row to all of its choices' rows.  SIZE: of an element.
-constexpr int kGatherPieces = 4;
-
-template <int SIZE>
+// A wave takes PIECES KB of a token's row to all of its choices' rows.  SIZE: of an element.
+template <int SIZE, int PIECES>
 __global__ __launch_bounds__(kMoeThreads) void k_moe_gather(const uint8_t* __restrict__ x, uint64_t ldx,
                                                             const int32_t* __restrict__ place, uint32_t T,
                                                             uint32_t K, uint32_t bytes, uint32_t R,
@@ -203,18 +201,18 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_gather(const uint8_t* __res
   const uint32_t t = __builtin_amdgcn_readfirstlane(blockIdx.x / spans * kMoeWaves + threadIdx.x / 64);
   if (t >= T) return;
   const Choices of(place, nullptr, t, K, R);
-  const uint32_t c = span * (kGatherPieces * 1024) + lane * 16;
+  const uint32_t c = span * (PIECES * 1024) + lane * 16;
   const uint8_t* from = x + (uint64_t)t * ldx;
-  u32x4 v[kGatherPieces];
+  u32x4 v[PIECES];
 #pragma unroll
-  for (int u = 0; u < kGatherPieces; ++u)
+  for (int u = 0; u < PIECES; ++u)
     if (c + u * 1024 < bytes) v[u] = *reinterpret_cast<const u32x4*>(from + c + u * 1024);
   for (uint32_t k = 0; k < K; ++k) {
     const uint32_t row = of.row_of(k);
     if (row == ~0u) continue;
     uint8_t* const to = out + (uint64_t)row * ldo;
 #pragma unroll
-    for (int u = 0; u < kGatherPieces; ++u) {
+    for (int u = 0; u < PIECES; ++u) {
       const uint32_t at = c + u * 1024;
       if (at + 16 <= bytes) {
         *reinterpret_cast<u32x4*>(to + at) = v[u];
@@ -266,18 +264,23 @@ hipError_t launch_moe_gather(uint64_t T, uint32_t K, uint64_t D, const s2r_mat& 
                              const s2r_q8_mat* outq, hipStream_t s) {
   const uint64_t size = x.dtype == S2R_F32 ? 4 : 2;
   if (out) {
-    const uint64_t spans = (D * size + kGatherPieces * 1024 - 1) / (kGatherPieces * 1024);
+    // a token's row in pieces of 4 KB to a wave, or of 1 KB where that leaves compute units without one (24
+    // tokens of 4 KB: 3.4 us, 4.6 in pieces of 4 KB)
+    const uint64_t bytes = D * size;
+    const bool few = T * ((bytes + 4095) / 4096) < 4 * 256;
+    const uint64_t spans = few ? (bytes + 1023) / 1024 : (bytes + 4095) / 4096;
     trace_mark(s, "k_moe_gather");
     by_rows(T, kMoeWaves, spans, [&](uint64_t t, uint64_t n) {
       const s2r_mat f = from_row(x, t);
       const dim3 grid((uint32_t)(spans * ((n + kMoeWaves - 1) / kMoeWaves)));
-#define S2R_GATHER(SIZE)                                                                             \
-  hipLaunchKernelGGL((k_moe_gather<SIZE>), grid, dim3(kMoeThreads), 0, s,                            \
+#define S2R_GATHER(SIZE, PIECES)                                                                     \
+  hipLaunchKernelGGL((k_moe_gather<SIZE, PIECES>), grid, dim3(kMoeThreads), 0, s,                    \
                      static_cast<const uint8_t*>(f.data), f.ld * size, place + t * K, (uint32_t)n, K, \
-                     (uint32_t)(D * size), (uint32_t)R, static_cast<uint8_t*>(out->data),            \
-                     out->ld * size, (uint32_t)spans)
-      if (size == 4) S2R_GATHER(4);
-      else S2R_GATHER(2);
+                     (uint32_t)bytes, (uint32_t)R, static_cast<uint8_t*>(out->data), out->ld * size, (uint32_t)spans)
+      if (size == 4 && few) S2R_GATHER(4, 1);
+      else if (size == 4) S2R_GATHER(4, 4);
+      else if (few) S2R_GATHER(2, 1);
+      else S2R_GATHER(2, 4);
 #undef S2R_GATHER
     });
   }

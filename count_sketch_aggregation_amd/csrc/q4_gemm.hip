@@ -2,7 +2,13 @@
 //   c[m][n] = sum_k a[m][k] sa[m][k / 32] b[n][k] sb[n][k / 32].
 // The scaled matrix instruction takes the codes and the scales as they are stored: a lane's 32 codes
 // of a fragment are one block.  Its first operand is B, so that a lane's results are consecutive columns of
-// C; one fp32 accumulator runs over the whole sum.
+// C; one fp32 accumulator runs over the whole sum.  Unlike in 8 bits it cuts nothing that fp32 would hold:
+// products of codes are multiples of 1/4 up to 36, and the eight neighbours that it adds first share
+// their scales.
+//
+// Measured on MI355X, 16384 x 8192 x 4096 to bf16: 295 us, 3.7 PFLOP/s; 4.8 with a sum of 16384, 6.1 if all
+// codes are zeros.  A chunk of 512 of a 256 x 256 tile takes 3.3 us, 2.6 for zeros, where its matrix instructions
+// take 4096 cycles: mostly power.  Results take 11 us a tile, in which all compute units write at once.
 #include <algorithm>
 
 #include "q4_device.hpp"
@@ -34,6 +40,7 @@ __device__ inline u32x4 q4_piece(const uint8_t* row, uint32_t k, uint32_t K) {
 template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_q4_gemm_few(s2r_q4_mat a, s2r_q4_mat b, s2r_mat c, uint32_t M,
                                                             uint32_t N, uint32_t K, uint32_t n_tiles) {
+  constexpr int kBatch = 2;  // steps of the sum a wave has in flight
   __shared__ f32x4 part[WAVES][64];
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
   const uint32_t n0 = blockIdx.x % n_tiles * 16, m0 = blockIdx.x / n_tiles * 16;
@@ -42,17 +49,33 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_gemm_few(s2r_q4_mat a, s2r_q4
   const uint8_t *scale_a = a.scale + m * a.lds, *scale_b = b.scale + n * b.lds;
   f32x4 acc = {};
   const uint32_t steps = (K + kQ4Step - 1) / kQ4Step;
-  for (uint32_t s = wave; s < steps; s += WAVES) {
-    const u32x2 sa = *reinterpret_cast<const u32x2*>(scale_a + 8 * s);
-    const u32x2 sb = *reinterpret_cast<const u32x2*>(scale_b + 8 * s);
+  for (uint32_t s = wave; s < steps; s += WAVES * kBatch) {
+    u32x4 fa[kBatch][2], fb[kBatch][2];
+    u32x2 sa[kBatch], sb[kBatch];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t k = s * kQ4Step + 128 * h + 32 * g;
-      const u32x4 fa = q4_piece(row_a, k, K), fb = q4_piece(row_b, k, K);
-      // codes beyond K are zeros, under whatever scale
-      const uint32_t xa = k < K ? sa[h] >> 8 * g : 127, xb = k < K ? sb[h] >> 8 * g : 127;
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q4_frag(fb), q4_frag(fa), acc, 4, 4, 0, (int)xb, 0,
-                                                             (int)xa);
+    for (int e = 0; e < kBatch; ++e) {
+      const uint32_t at = s + e * WAVES;
+      if (at >= steps) continue;
+      sa[e] = *reinterpret_cast<const u32x2*>(scale_a + 8 * at);
+      sb[e] = *reinterpret_cast<const u32x2*>(scale_b + 8 * at);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t k = at * kQ4Step + 128 * h + 32 * g;
+        fa[e][h] = q4_piece(row_a, k, K), fb[e][h] = q4_piece(row_b, k, K);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const uint32_t at = s + e * WAVES;
+      if (at >= steps) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // codes beyond K are zeros, under whatever scale
+        const bool in = at * kQ4Step + 128 * h + 32 * g < K;
+        const uint32_t xa = in ? sa[e][h] >> 8 * g : 127, xb = in ? sb[e][h] >> 8 * g : 127;
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q4_frag(fb[e][h]), q4_frag(fa[e][h]), acc, 4, 4, 0,
+                                                               (int)xb, 0, (int)xa);
+      }
     }
   }
   part[wave][lane] = acc;
@@ -351,26 +374,29 @@ __global__ __launch_bounds__(kQ4SumThreads) void k_q4_gemm_sum(const float* __re
 
 namespace {
 
-// Tiles and parts of the sum with the least estimated time, in nanoseconds: a chunk of 512 of the sum, the
-// beginning and the end of a tile, in rounds over the compute units.  Parts are written and read again, at 4
-// bytes a picosecond, by a launch of 3000.
+// Tiles and parts of the sum with the least estimated time, in nanoseconds: of 256 x 256 a compute unit takes one,
+// 3400 for a chunk of the sum and 12000 to begin and to leave (results leave all compute units at once); of 128 x
+// 128 it takes one in 1380 and 3500 or two beside each other in 2520 and 4400.  Parts are written and read again,
+// at 4 bytes a picosecond, by a launch of 3000.  Measured, tiles of 256 and of 128: 4096 x 4096 x 4096 41 us and
+// 51, 5001 x 1000 x 4100 39 and 29, 2048 x 2048 x 4096 28 and 16; tiles of 256 x 128 were best nowhere.
 struct Q4Plan {
-  uint32_t tm, tn, mt, nt, chunks;
+  uint32_t side, mt, nt, chunks;
   Cut cut;  // in chunks
 };
 Q4Plan q4_plan(uint64_t M, uint64_t N, uint64_t K) {
-  static constexpr uint32_t kTiles[][4] = {{256, 256, 2400, 8000}, {256, 128, 1700, 6000}, {128, 128, 1300, 5000}};
   const uint32_t chunks = (uint32_t)((K + kQ4Chunk - 1) / kQ4Chunk);
   Q4Plan best = {};
   uint64_t least = ~0ull;
-  for (const auto& t : kTiles) {
-    Q4Plan p = {t[0], t[1], (uint32_t)((M + t[0] - 1) / t[0]), (uint32_t)((N + t[1] - 1) / t[1]), chunks, {1, chunks}};
+  for (const uint32_t side : {256u, 128u}) {
+    Q4Plan p = {side, (uint32_t)((M + side - 1) / side), (uint32_t)((N + side - 1) / side), chunks, {1, chunks}};
     const uint64_t tiles = (uint64_t)p.mt * p.nt;
     for (uint32_t parts = 1; parts <= 16; ++parts) {
       p.cut = cut_evenly(chunks, parts);
-      if (parts > 1 && (p.cut.parts != parts || tiles * parts > kTileCus)) continue;
-      const uint64_t rounds = (tiles * parts + kTileCus - 1) / kTileCus;
-      uint64_t ns = rounds * ((uint64_t)p.cut.blocks * t[2] + t[3]);
+      const uint64_t all = tiles * parts, each = p.cut.blocks;
+      if (parts > 1 && (p.cut.parts != parts || all > kTileCus)) continue;
+      uint64_t ns = side == 256         ? (all + kTileCus - 1) / kTileCus * (each * 3400 + 12000)
+                    : all <= kTileCus ? each * 1380 + 3500
+                                        : (all + 2 * kTileCus - 1) / (2 * kTileCus) * (each * 2520 + 4400);
       if (parts > 1) ns += 3000 + M * N * 4 * (2 * parts + 1) / 4000;
       if (ns < least) least = ns, best = p;
     }
@@ -378,6 +404,7 @@ Q4Plan q4_plan(uint64_t M, uint64_t N, uint64_t K) {
   return best;
 }
 
+// 33 x 4096 x 4096 takes 9.5 us as few rows and 10.2 in tiles, 64 13.0 and 11.1.
 bool q4_few_rows(uint64_t M) { return M <= 32; }
 
 }  // namespace
@@ -404,20 +431,16 @@ hipError_t launch_q4_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q4_mat& 
   if (cut) out = {workspace, (N + 3) / 4 * 4, S2R_F32};
   const uint64_t part_bytes = M * out.ld * sizeof(float);
   const uint32_t total = p.mt * p.nt * p.cut.parts;
-  const dim3 grid(std::min(total, kTileCus));
-#define S2R_TILE(FM, FN)                                                                                         \
-  do {                                                                                                           \
-    if (k % kQ4Chunk == 0)                                                                                       \
-      hipLaunchKernelGGL((k_q4_gemm<2, 2, FM, FN, false>), grid, dim3(256), 0, s, a, b, out, part_bytes, m, n, k, \
-                         p.mt, p.nt, total, 2 * p.cut.blocks);                                                   \
-    else                                                                                                         \
-      hipLaunchKernelGGL((k_q4_gemm<2, 2, FM, FN, true>), grid, dim3(256), 0, s, a, b, out, part_bytes, m, n, k,  \
-                         p.mt, p.nt, total, 2 * p.cut.blocks);                                                   \
-  } while (0)
+  const dim3 grid(std::min(total, p.side == 128 ? 2 * kTileCus : kTileCus));
+#define S2R_TILE(F, TAIL)                                                                                      \
+  hipLaunchKernelGGL((k_q4_gemm<2, 2, F, F, TAIL>), grid, dim3(256), 0, s, a, b, out, part_bytes, m, n, k, p.mt, \
+                     p.nt, total, 2 * p.cut.blocks)
   trace_mark(s, "k_q4_gemm");
-  if (p.tn == 256) S2R_TILE(4, 4);
-  else if (p.tm == 256) S2R_TILE(4, 2);
-  else S2R_TILE(2, 2);
+  const bool tail = k % kQ4Chunk != 0;
+  if (p.side == 256 && tail) S2R_TILE(4, true);
+  else if (p.side == 256) S2R_TILE(4, false);
+  else if (tail) S2R_TILE(2, true);
+  else S2R_TILE(2, false);
 #undef S2R_TILE
   if (cut) {
     trace_mark(s, "k_q4_gemm_sum");

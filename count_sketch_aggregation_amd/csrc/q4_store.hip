@@ -35,22 +35,20 @@ __device__ inline void q4_store16(uint8_t* row, uint32_t c, uint32_t cols, u32x2
 }
 
 // ---- rows ---------------------------------------------------------------------------------
-// 16 elements to a lane, 2 lanes to a block, 64 lanes to 1024 columns; kSaveRows rows to a wave.
-constexpr int kSaveRows = 4;
-
-template <int DT>
+// 16 elements to a lane, 2 lanes to a block, 64 lanes to 1024 columns; ROWS rows to a wave.
+template <int DT, int ROWS>
 __global__ __launch_bounds__(kQ4Threads) void k_q4_save(s2r_mat x, s2r_q4_mat out, uint32_t R, uint32_t C,
                                                         uint32_t spans) {
   const uint32_t span = blockIdx.x % spans, lane = threadIdx.x % 64;
-  const uint32_t r0 = (blockIdx.x / spans * (kQ4Threads / 64) + threadIdx.x / 64) * kSaveRows;
+  const uint32_t r0 = (blockIdx.x / spans * (kQ4Threads / 64) + threadIdx.x / 64) * ROWS;
   const uint32_t c = span * 1024 + lane * 16;
-  Raw16<DT> raw[kSaveRows];
+  Raw16<DT> raw[ROWS];
 #pragma unroll
-  for (int i = 0; i < kSaveRows; ++i)
+  for (int i = 0; i < ROWS; ++i)
     raw[i] = load_raw16<DT>(static_cast<const uint8_t*>(x.data) +
                                 (uint64_t)min(r0 + i, R - 1) * x.ld * elem_bytes<DT>(), c, C);
 #pragma unroll
-  for (int i = 0; i < kSaveRows; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     float v[16];
     unpack16<DT>(raw[i], v);
     const uint32_t b = q4_scale_byte(max_over_2(bits16(v)));
@@ -195,14 +193,22 @@ hipError_t launch_q4_save(uint64_t R, uint64_t C, const s2r_mat& x, const s2r_q4
     });
     return hipGetLastError();
   }
-  const uint64_t spans = (C + 1023) / 1024, each = kQ4Threads / 64 * kSaveRows;
+  // four rows to a wave, or one where that leaves compute units without work (1001 x 1000 fp32: S2R_A us, S2R_B with
+  // four)
+  const uint64_t spans = (C + 1023) / 1024;
+  const bool few = spans * ((R + 15) / 16) < 2 * 256;
+  const uint64_t each = kQ4Threads / 64 * (few ? 1 : 4);
   trace_mark(s, "k_q4_save");
   by_rows(R, each, spans, [&](uint64_t r, uint64_t n) {
     const s2r_mat f = from_row(x, r);
     const s2r_q4_mat o = from_row(*out, r);
     const dim3 grid((uint32_t)(spans * ((n + each - 1) / each)));
-    S2R_Q4_TYPES(x.dtype, hipLaunchKernelGGL((k_q4_save<DT>), grid, dim3(kQ4Threads), 0, s, f, o, (uint32_t)n,
-                                             (uint32_t)C, (uint32_t)spans));
+#define S2R_SAVE(ROWS)                                                                                         \
+  S2R_Q4_TYPES(x.dtype, hipLaunchKernelGGL((k_q4_save<DT, ROWS>), grid, dim3(kQ4Threads), 0, s, f, o, (uint32_t)n, \
+                                           (uint32_t)C, (uint32_t)spans))
+    if (few) S2R_SAVE(1);
+    else S2R_SAVE(4);
+#undef S2R_SAVE
   });
   return hipGetLastError();
 }

@@ -33,38 +33,64 @@ __device__ inline ExpertRows nth_expert(const s2r_experts& e, uint32_t M, uint32
   return {~0u, 0, 0};
 }
 
-template <int FA, int FB, int WAVES>
+// NF: fragments of 16 columns to a workgroup.  Rows go 32 at a time, the upper 16 where there are any.
+template <int FA, int FB, int NF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few_experts(s2r_q8_mat a, s2r_q8_mat b, ExpertSteps steps,
                                                                     s2r_mat c, s2r_experts experts, uint32_t M,
                                                                     uint32_t N, uint32_t K) {
-  __shared__ f32x4 part[WAVES][64];
+  __shared__ f32x4 part[WAVES][2][NF][64];
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
-  const uint32_t n0 = blockIdx.x * 16, n = min(n0 + r, N - 1);
+  const uint32_t n0 = blockIdx.x * (16 * NF);
   const uint32_t blocks = (K + kQ8Block - 1) / kQ8Block;
   for (uint32_t nth = blockIdx.y;; nth += gridDim.y) {
     const ExpertRows x = nth_expert(experts, M, nth);
     if (x.expert == ~0u) return;
-    const uint8_t* row_b = b.q + x.expert * steps.step + (uint64_t)n * b.ld;
-    const uint8_t* scale_b = b.scale + x.expert * steps.scale_step + n0 / kQ8Block;
-    for (uint32_t m0 = x.first; m0 < x.end; m0 += 16) {
-      const uint32_t m = min(m0 + r, x.end - 1);
-      const uint8_t* row_a = a.q + (uint64_t)m * a.ld;
-      f32x4 acc = {};
+    const uint8_t* const expert_b = b.q + x.expert * steps.step;
+    const uint8_t* const scale_b = b.scale + x.expert * steps.scale_step + n0 / kQ8Block;  // of all 16 NF columns
+    static_assert(kQ8Block % (16 * NF) == 0, "");
+    for (uint32_t m0 = x.first; m0 < x.end; m0 += 32) {
+      const bool two = m0 + 16 < x.end;
+      const uint32_t m[2] = {min(m0 + r, x.end - 1), min(m0 + 16 + r, x.end - 1)};
+      f32x4 acc[2][NF] = {};
       for (uint32_t s = wave; s < blocks; s += WAVES) {
         const uint32_t k = s * kQ8Block + 16 * g;
-        const i32x8 fb = load_frag(row_b, k, K), fa = load_frag(row_a, k, K);
-        const uint32_t sb = scale_b[(uint64_t)s * b.lds], sa = a.scale[(uint64_t)s * a.lds + m];
+        i32x8 fb[NF], fa[2];
+        uint32_t sa[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<FB>(fb, p, sb), widen8<FA>(fa, p, sa), acc, 0, 0, 0);
+        for (int f = 0; f < NF; ++f) fb[f] = load_frag(expert_b + (uint64_t)min(n0 + 16 * f + r, N - 1) * b.ld, k, K);
+        const uint32_t sb = scale_b[(uint64_t)s * b.lds];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !two) continue;
+          fa[i] = load_frag(a.q + (uint64_t)m[i] * a.ld, k, K);
+          sa[i] = a.scale[(uint64_t)s * a.lds + m[i]];
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          bf16x8 wb[NF];
+#pragma unroll
+          for (int f = 0; f < NF; ++f) wb[f] = widen8<FB>(fb[f], p, sb);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i == 1 && !two) continue;
+            const bf16x8 wa = widen8<FA>(fa[i], p, sa[i]);
+#pragma unroll
+            for (int f = 0; f < NF; ++f) acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[f], wa, acc[i][f], 0, 0, 0);
+          }
+        }
       }
-      part[wave][lane] = acc;
-      __syncthreads();
-      if (wave == 0) {
-        f32x4 v = part[0][lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += part[w][lane];
-        if (m0 + r < x.end && n0 + 4 * g < N) store4(c, m0 + r, n0 + 4 * g, N, v);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) part[wave][i][f][lane] = acc[i][f];
+      __syncthreads();
+      for (uint32_t e = threadIdx.x; e < (two ? 2 : 1) * NF * 64; e += 64 * WAVES) {
+        const uint32_t i = e / (NF * 64), f = e / 64 % NF, l = e % 64;
+        f32x4 v = part[0][i][f][l];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v += part[w][i][f][l];
+        const uint32_t row = m0 + 16 * i + l % 16, col = n0 + 16 * f + l / 16 * 4;
+        if (row < x.end && col < N) store4(c, row, col, N, v);
       }
       __syncthreads();
     }
@@ -73,32 +99,47 @@ __global__ __launch_bounds__(64 * WAVES) void k_q8_gemm_few_experts(s2r_q8_mat a
 
 namespace {
 
-// A few rows to an expert are summed as few rows are; more go to tiles, whose height the average tells
-// (how many rows an expert has, the host does not know).
+// A few rows to an expert are summed as few rows are, more go to tiles; the host knows only how many there are on
+// average (M is at most 20 for each: 100 tokens of 4 choices, 32 experts of 2048 x 2048 38 us, 41 in tiles; 200
+// tokens 57 and 38).
 template <int FA, int FB>
 void go_gemm_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, const s2r_q8_mat& a,
                      const s2r_q8_mat& b, ExpertSteps steps, const s2r_mat& c, hipStream_t s) {
   const uint32_t m = (uint32_t)M, n = (uint32_t)N, k = (uint32_t)K;
-  if (M <= 32 * (uint64_t)e.experts) {
+  if (M <= 20 * (uint64_t)e.experts) {
     // experts with rows are at least 4 rows apart
-    const dim3 grid((n + 15) / 16, (uint32_t)std::min<uint64_t>(e.experts, (M + 3) / 4));
+    const uint32_t some = (uint32_t)std::min<uint64_t>(e.experts, (M + 3) / 4);
     trace_mark(s, "k_q8_gemm_few_experts");
-    hipLaunchKernelGGL((k_q8_gemm_few_experts<FA, FB, 8>), grid, dim3(512), 0, s, a, b, steps, c, e, m, n, k);
+    const dim3 grid((n + 31) / 32, some);
+    // two workgroups for every compute unit or fewer: more waves each (2 experts of 4096 x 4096, one token: 10 us
+    // with 8, 13 with 4; 60 of 2048 x 2048, 64 tokens: 65 and 56)
+    if ((uint64_t)grid.x * some <= 2 * kTileCus)
+      hipLaunchKernelGGL((k_q8_gemm_few_experts<FA, FB, 2, 8>), grid, dim3(512), 0, s, a, b, steps, c, e, m, n, k);
+    else
+      hipLaunchKernelGGL((k_q8_gemm_few_experts<FA, FB, 2, 4>), grid, dim3(256), 0, s, a, b, steps, c, e, m, n, k);
     return;
   }
+  // Tiles by estimated time, in nanoseconds: of 256 x 256 one to a compute unit, 2700 for a block of the sum and
+  // 8000 to begin and to leave; of 128 x 128 two beside each other, 1500 and 4500 (8192 tokens of 4 choices, 16
+  // experts of 4096 x 2048: 456 us and 489; 2 choices, 8 of 2048 x 2048: 148 and 130).  As many
+  // tiles are reckoned with as there can be, for some experts have many more rows than others (4000 tokens of one
+  // choice, 32 experts of 2048 x 1024: 53 and 33).
   const uint32_t blocks = (k + kQ8Block - 1) / kQ8Block;
-  auto tiles = [&](uint64_t tm, uint64_t tn) { return (M / tm + std::min<uint64_t>(e.experts, M / 4)) * ((N + tn - 1) / tn); };
+  const uint64_t some = std::min<uint64_t>(e.experts, M / 4);
+  auto tiles = [&](uint64_t side) { return (M / side + some) * ((N + side - 1) / side); };
+  auto rounds = [](uint64_t n, uint64_t width) { return (n + width - 1) / width; };
+  const bool large = rounds(tiles(256), kTileCus) * (blocks * 2700 + 8000) < rounds(tiles(128), 2 * kTileCus) * (blocks * 1500 + 4500);
+  const dim3 grid((uint32_t)(large ? std::min<uint64_t>(tiles(256), kTileCus) : std::min<uint64_t>(tiles(128), 2 * kTileCus)));
 #define S2R_TILE(FM, FN, TAIL)                                                                                   \
-  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, FM, FN, TAIL, true, true>),                                        \
-                     dim3((uint32_t)std::min<uint64_t>(tiles(64 * FM, 64 * FN), kTileCus)), dim3(256), 0, s, a, b, c, 0, m, \
-                     n, k, 0, (n + 64 * FN - 1) / (64 * FN), 0, blocks, ExpertTiles{e, steps})
+  hipLaunchKernelGGL((k_q8_gemm<FA, FB, 2, 2, FM, FN, TAIL, true, true>), grid, dim3(256), 0, s, a, b, c, 0, m, n, k, 0, \
+                     (n + 64 * FN - 1) / (64 * FN), 0, blocks, ExpertTiles{e, steps})
 #define S2R_TILE_TAIL(FM, FN)                          \
   do {                                                 \
     if (k % kQ8Block == 0) S2R_TILE(FM, FN, false);    \
     else S2R_TILE(FM, FN, true);                       \
   } while (0)
   trace_mark(s, "k_q8_gemm_experts");
-  if (tiles(256, 256) >= kTileCus && M >= 192 * (uint64_t)e.experts) S2R_TILE_TAIL(4, 4);
+  if (large) S2R_TILE_TAIL(4, 4);
   else S2R_TILE_TAIL(2, 2);
 #undef S2R_TILE_TAIL
 #undef S2R_TILE
