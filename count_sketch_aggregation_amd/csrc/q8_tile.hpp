@@ -67,7 +67,9 @@ __device__ inline void sync_reads() {
 // Item b of `total` to a tile and a part of the sum.  Consecutive workgroups go to the eight
 // accelerator dies in turn, so the items are cut into eight stretches, one for each die and
 // its L2; within a stretch kTileGroup rows of tiles are walked column by column, so that the
-// workgroups that run together on a die share rows and columns of both operands.
+// workgroups that run together on a die share rows and columns of both operands.  The dies begin an
+// eighth of the columns apart, so that the lines they write at a time lie on different memory channels
+// (4-bit product 16384 x 8192 x 4096: to bf16 280 us, 290 without; to fp32 347 and 402).
 struct TileAt {
   uint32_t row, col, part;
 };
@@ -80,7 +82,8 @@ __device__ inline TileAt tile_at(uint32_t b, uint32_t rows, uint32_t cols, uint3
   const uint32_t span = kTileGroup * cols, g = lin / span, first = g * kTileGroup;
   const uint32_t height = min(rows - first, kTileGroup), in = lin - g * span;
   t.row = first + in % height;
-  t.col = in / height;
+  t.col = in / height + die * cols / kXcds;
+  t.col = t.col < cols ? t.col : t.col - cols;
   // divisions run in vector registers: back to scalar ones
   t.row = __builtin_amdgcn_readfirstlane(t.row);
   t.col = __builtin_amdgcn_readfirstlane(t.col);
@@ -119,15 +122,20 @@ __device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, ui
     for (uint32_t e = 0; e < 8; ++e) *reinterpret_cast<f32x4_a4*>(at + 4 * e * ld) = v[e];
     return;
   }
+  // ragged: what is there is read at once, then added to
+  float old[8][4] = {};
+  if (accumulate) {
 #pragma unroll
-  for (uint32_t e = 0; e < 8; ++e) {
-    if (n0 + lane / 16 + 4 * e >= N) continue;
+    for (uint32_t e = 0; e < 8; ++e)
 #pragma unroll
-    for (uint32_t c = 0; c < 4; ++c) {
-      float* const p = at + 4 * e * ld + c;
-      if (k + c < K) *p = accumulate ? *p + v[e][c] : v[e][c];
-    }
+      for (uint32_t c = 0; c < 4; ++c)
+        if (n0 + lane / 16 + 4 * e < N && k + c < K) old[e][c] = at[4 * e * ld + c];
   }
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e)
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      if (n0 + lane / 16 + 4 * e < N && k + c < K) at[4 * e * ld + c] = accumulate ? old[e][c] + v[e][c] : v[e][c];
 }
 
 // 16-byte piece s of a 128-byte LDS row p lies at s ^ spread(p): the 32 lanes that read one piece of
