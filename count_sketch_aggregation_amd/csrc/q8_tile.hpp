@@ -122,20 +122,35 @@ __device__ inline void add_turned(float* dw, uint64_t ld, const uint8_t* lds, ui
     for (uint32_t e = 0; e < 8; ++e) *reinterpret_cast<f32x4_a4*>(at + 4 * e * ld) = v[e];
     return;
   }
-  // ragged: what is there is read at once, then added to
-  float old[8][4] = {};
+  // ragged: what is there is read at once, then added to; four columns together where the row has them
+  const bool four = k + 4 <= K;
   if (accumulate) {
+    f32x4 old[8] = {};
 #pragma unroll
-    for (uint32_t e = 0; e < 8; ++e)
+    for (uint32_t e = 0; e < 8; ++e) {
+      if (n0 + lane / 16 + 4 * e >= N) continue;
+      if (four) {
+        old[e] = *reinterpret_cast<const f32x4_a4*>(at + 4 * e * ld);
+      } else {
 #pragma unroll
-      for (uint32_t c = 0; c < 4; ++c)
-        if (n0 + lane / 16 + 4 * e < N && k + c < K) old[e][c] = at[4 * e * ld + c];
+        for (uint32_t c = 0; c < 3; ++c)
+          if (k + c < K) old[e][c] = at[4 * e * ld + c];
+      }
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e) v[e] += old[e];
   }
 #pragma unroll
-  for (uint32_t e = 0; e < 8; ++e)
+  for (uint32_t e = 0; e < 8; ++e) {
+    if (n0 + lane / 16 + 4 * e >= N) continue;
+    if (four) {
+      *reinterpret_cast<f32x4_a4*>(at + 4 * e * ld) = v[e];
+    } else {
 #pragma unroll
-    for (uint32_t c = 0; c < 4; ++c)
-      if (n0 + lane / 16 + 4 * e < N && k + c < K) at[4 * e * ld + c] = accumulate ? old[e][c] + v[e][c] : v[e][c];
+      for (uint32_t c = 0; c < 3; ++c)
+        if (k + c < K) at[4 * e * ld + c] = v[e][c];
+    }
+  }
 }
 
 // 16-byte piece s of a 128-byte LDS row p lies at s ^ spread(p): the 32 lanes that read one piece of
