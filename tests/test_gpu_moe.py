@@ -415,3 +415,46 @@ def test_a_layer_and_its_gradients():
         # stored in e5m2 each is off by at most 2^-3, on average by half of that or less
         assert float((gw[e].double() - vw.grad[e]).norm()) <= 2.0 ** -4 * float(vw.grad[e].norm()) + 1e-30
     assert bool((g.codes[~m.used.to(DEV)] == q8.POISON).all())
+
+
+def test_rows_beyond_four_gib():
+    """Rows whose offsets do not fit 32 bits, in every call that goes by rows."""
+    gp.say("rows beyond 4 GiB")
+    T, K, D, R = 70, 2, 4096, 1_100_000  # 4.5 GB of codes, 9 GB of bf16
+    far = R - 200
+    place = (far + torch.randperm(T * K, generator=q8._gen(1)).view(T, K)).int().to(DEV)
+    x = torch.randn((T, D), generator=q8._gen(2)).bfloat16()
+    src = s2r.mat(q8.wide(T, D, "bf16", x=x)[:, :D])
+    rows = torch.empty((R, D), dtype=torch.bfloat16, device=DEV)
+    q = s2r.alloc_q8(R, D)
+    s2r.s2r_moe_gather(T, K, D, src, place, R, s2r.mat(rows), q)
+    at = place.long().view(-1)
+    per = x[torch.arange(T).repeat_interleave(K)]
+    assert torch.equal(rows[at].cpu(), per)
+    codes, b = ref.quantise(per, "e4m3")
+    assert torch.equal(ref.code_values("e4m3")[q.codes[at][:, :D].cpu().int()], codes)
+    assert torch.equal(q.scales[:, at].cpu().t().long(), b)
+    y = q8.wide(T, D, "f32", fill=7.0)
+    s2r.s2r_moe_combine(T, K, D, s2r.mat(rows), R, place, None, s2r.mat(y))
+    assert torch.equal(y[:, :D].cpu(), K * x.float())
+    dw = torch.zeros((T, K), device=DEV)
+    s2r.s2r_moe_combine_grad(T, K, D, src, place, R, rows=s2r.mat(rows), drowsq=q, dweight=dw)
+    want = (x.double() ** 2).sum(1)
+    assert bool(((dw.cpu().double() - want[:, None]).abs() <= D * 2.0 ** -24 * want[:, None]).all())
+    # two experts on those rows: 100 and 40, then 8 and 4, as few rows and as tiles have them
+    v = torch.zeros((R - far, D), dtype=torch.float64)
+    v[at.cpu() - far] = codes * ref.spread(b, T * K, D, False)
+    w, vw = q8.integers(256, D, "e4m3", 3, True)
+    for n0, n1 in ((100, 40), (8, 4)):
+        e = s2r.experts(torch.tensor([far, far + n0], dtype=torch.int32, device=DEV), torch.tensor([n0, n1], dtype=torch.int32, device=DEV))
+        want = torch.cat([v[:n0] @ vw[:128].t(), v[n0:n0 + n1] @ vw[128:].t()])
+        mass = torch.cat([v[:n0].abs() @ vw[:128].abs().t(), v[n0:n0 + n1].abs() @ vw[128:].abs().t()])
+        c = torch.empty((R, 128), device=DEV)
+        s2r.s2r_q8_gemm_experts(R, 128, D, e, q, w, 128 * w.ld, 1, s2r.mat(c))
+        assert bool(((c[far:far + n0 + n1].cpu().double() - want).abs() <= D * 2.0 ** -23 * mass).all())
+        dw = torch.empty((2, 64, D), device=DEV)
+        s2r.s2r_q8_wgrad_experts(R, 64, D, e, s2r.mat(rows[:, :64]), q, dw, D, 64 * D)
+        dy = rows[far:far + n0 + n1, :64].cpu().double()
+        for i, (f, n) in enumerate(((0, n0), (n0, n1))):
+            want, mass = dy[f:f + n].t() @ v[f:f + n], dy[f:f + n].abs().t() @ v[f:f + n].abs()
+            assert bool(((dw[i].cpu().double() - want).abs() <= (n * 2.0 ** -23) * mass + 2.0 ** -140).all())

@@ -247,3 +247,69 @@ def test_a_layers_three_products(M, K, N):
         want, mass = v[va] @ v[vb].t(), v[va].abs() @ v[vb].abs().t()
         got = product(P, Q, S, a, b, "f32", True).double()
         assert bool(((got - want).abs() <= S * 2.0 ** -23 * mass + 2.0 ** -24 * want.abs()).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 300, 1000), (300, 1000, 4096), (900, 700, 600)])
+def test_graph_replays_and_other_streams(M, N, K):
+    """Storage and product, with a cut sum among them: the same bits eager, on another stream and from every replay of a
+    graph, with eager work between the replays."""
+    gp.say(f"q4 graph {M}x{N}x{K}")
+
+    def keep(seed):
+        g = q8._gen(seed)
+        x, w = (torch.randn((r, K), generator=g).bfloat16() for r in (M, N))
+        return dict(x=s2r.mat(q8.wide(M, K, "bf16", x=x)[:, :K]), w=s2r.mat(q8.wide(N, K, "bf16", x=w)[:, :K]),
+                    xq=s2r.alloc_q4(M, K), xt=s2r.alloc_q4(K, M), wq=s2r.alloc_q4(N, K), y=torch.zeros((M, up(N, 8)), device=DEV),
+                    ws=q8.workspace(s2r.s2r_q4_gemm_workspace_bytes(M, N, K)))
+
+    def step(k, stream=None):
+        s2r.s2r_q4_save(M, K, k["x"], k["xq"], k["xt"], stream=stream)
+        s2r.s2r_q4_save(N, K, k["w"], k["wq"], stream=stream)
+        s2r.s2r_q4_gemm(M, N, K, k["xq"], k["wq"], s2r.mat(k["y"][:, :N]), workspace=k["ws"], stream=stream)
+
+    k, other = keep(1), keep(2)
+    step(k)
+    want = k["y"].clone()
+    side = torch.cuda.Stream()
+    k["y"].fill_(0)
+    torch.cuda.synchronize()
+    step(k, side)
+    torch.cuda.synchronize()
+    assert torch.equal(k["y"][:, :N], want[:, :N])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(k)
+    for rep in range(3):
+        for t in (k["y"], k["xq"].codes, k["xq"].scales, k["wq"].codes):
+            t.fill_(5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(k["y"][:, :N], want[:, :N]), rep
+        step(other)
+
+
+def test_rows_beyond_four_gib():
+    """Codes and results whose offsets do not fit 32 bits: the last rows of a long matrix."""
+    gp.say("q4 beyond 4 GiB")
+    M, N, K = 1_100_000, 1000, 8192  # 4.5 GB of codes, 4.4 GB of fp32 results
+    a = s2r.alloc_q4(M, K)
+    a.codes.zero_(), a.scales.fill_(127)
+    b, vb = exact_matrix(N, K, 2)
+    n = 300
+    code = torch.randint(0, 5, (n, K), generator=q8._gen(3)) + 8 * torch.randint(0, 2, (n, K), generator=q8._gen(4))
+    a.codes[-n:] = (code[:, 0::2] | code[:, 1::2] << 4).to(torch.uint8).to(DEV)
+    va = ref4.code_values()[code]
+    c = torch.empty((M, N), device=DEV)
+    s2r.s2r_q4_gemm(M, N, K, a, b, s2r.mat(c))
+    assert torch.equal(c[-n:].cpu(), va.float() @ vb.float().t())
+    assert bool((c[:-n] == 0).all())
+    y = c.view(torch.bfloat16)[:, :K // 8]
+    s2r.s2r_q4_load(M, K // 8, a, s2r.mat(y))
+    assert torch.equal(y[-n:].cpu().double(), va[:, :K // 8])
+    again = s2r.alloc_q4(M, K // 8)
+    s2r.s2r_q4_save(M, K // 8, s2r.mat(y), again)
+    back = torch.empty((n, K // 8), dtype=torch.bfloat16, device=DEV)
+    tail = s2r.q4_mat(again.codes[-n:], again.scales[-n:])
+    s2r.s2r_q4_load(n, K // 8, tail, s2r.mat(back))
+    assert torch.equal(back.cpu().double(), va[:, :K // 8])
