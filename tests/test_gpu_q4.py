@@ -313,3 +313,27 @@ def test_rows_beyond_four_gib():
     tail = s2r.q4_mat(again.codes[-n:], again.scales[-n:])
     s2r.s2r_q4_load(n, K // 8, tail, s2r.mat(back))
     assert torch.equal(back.cpu().double(), va[:, :K // 8])
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_product_keeps_small_products_beside_large_ones(M):
+    """2^12 in one block of the sum and multiples of 2^-11 in every other one: fp32 holds all of it, wherever the
+    instruction adds them."""
+    gp.say(f"q4 gemm small beside large M={M}")
+    N, K = 140, 600
+    nb = up(K, 32) // 32
+    for big in (0, 3, 5, 18):
+        g = q8._gen(big)
+        ca, cb = torch.zeros((M, K), dtype=torch.long), torch.zeros((N, K), dtype=torch.long)
+        ba, bb = torch.full((M, nb), 127 - 4), torch.full((N, nb), 127 - 5)
+        at = torch.arange(nb) * 32 + torch.randint(0, 24, (nb,), generator=g)
+        ca[:, at] = torch.randint(0, 2, (M, nb), generator=g)           # 0 or 1/2, times 2^-4
+        cb[:, at] = torch.randint(0, 2, (N, nb), generator=g) * (1 + 8 * torch.randint(0, 2, (N, nb), generator=g))
+        ca[:, big * 32:big * 32 + 32], cb[:, big * 32:big * 32 + 32] = 0, 0
+        ca[:, big * 32 + 7], cb[:, big * 32 + 7] = 6, 6                 # 4, times 2^4
+        ba[:, big], bb[:, big] = 127 + 4, 127 + 4
+        want = ref4.values(ca, ba) @ ref4.values(cb, bb).t()
+        assert len(want.unique()) > 2 and float((want * 2 ** 11).frac().abs().max()) == 0
+        a, b = stored(ca, ba), stored(cb, bb)
+        for with_ws in (False, True):
+            assert torch.equal(product(M, N, K, a, b, "f32", with_ws).double(), want), (big, with_ws)
