@@ -457,23 +457,28 @@ def s2r_q8_glu_grad(M: int, F: int, act, gq: s2r_q8_mat, uq: s2r_q8_mat | None, 
 # layers of experts (include/s2r_moe.h)
 
 
-def _dense(t, shape: tuple, dtypes: tuple, where: str):
-    """Device pointer of a dense tensor of `shape` (None and addresses pass through)."""
-    if t is None or isinstance(t, int):
+_DTYPES: dict = {}  # torch's types by name, once torch is there
+
+
+def _dense(t, shape: tuple, kind: str, where: str):
+    """Device pointer of a dense tensor of `shape` and of the types "ints" or "floats" (None and
+    addresses pass through)."""
+    if t is None or type(t) is int:
         return t
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+    if not _DTYPES:
+        import torch
+        _DTYPES.update(ints=(torch.int32, torch.uint32), floats=(torch.float32,))
+    if t.dtype not in _DTYPES[kind] or t.shape != shape or not t.is_contiguous():
         raise S2RError(S2R_ERR_DIM, where)
     return t.data_ptr()
 
 
 def _ints(t, shape: tuple, where: str):
-    import torch
-    return _dense(t, shape, (torch.int32, torch.uint32), where)
+    return _dense(t, shape, "ints", where)
 
 
 def _floats(t, shape: tuple, where: str):
-    import torch
-    return _dense(t, shape, (torch.float32,), where)
+    return _dense(t, shape, "floats", where)
 
 
 def experts(first, rows) -> s2r_experts:

@@ -7,6 +7,7 @@
 // (5.3 and more); 1001 x 1000 fp32 3.1, and back to bf16 3.2.
 #include "q4_device.hpp"
 #include "q4_launch.hpp"
+#include "q8_tile.hpp"
 
 namespace s2r {
 
@@ -72,7 +73,8 @@ __global__ __launch_bounds__(kQ4Threads) void k_q4_save_both(s2r_mat x, s2r_q4_m
   // 16 bytes more than a row: the lanes of a write, 8 to a row, meet the banks evenly
   constexpr int kStride = kSide + 16 / sizeof(E);
   __shared__ __attribute__((aligned(16))) E tile[kSide * kStride];
-  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles, t = threadIdx.x;
+  const TileAt tile_of = tile_at(blockIdx.x, gridDim.x / col_tiles, col_tiles, gridDim.x);
+  const uint32_t ct = tile_of.col, rt = tile_of.row, t = threadIdx.x;
   const uint32_t c = ct * kSide + t % 8 * 16;
   Raw16<DT> raw[4];
 #pragma unroll
