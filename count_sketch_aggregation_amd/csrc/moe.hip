@@ -336,11 +336,8 @@ __device__ inline void load8(const uint8_t* row, uint32_t c, uint32_t cols, floa
   }
 }
 
-// A wave takes kCombinePieces x 512 columns of a token, eight to a lane at a time, and reads
-// kCombineRows of its rows at once.
-constexpr int kCombinePieces = 2, kCombineRows = 4;
-
-template <int DT>
+// A wave takes PIECES x 512 columns of a token, eight to a lane at a time, and reads ROWS of its rows at once.
+template <int DT, int PIECES, int ROWS>
 __global__ __launch_bounds__(kMoeThreads) void k_moe_combine(s2r_mat rows, uint32_t R,
                                                              const int32_t* __restrict__ place,
                                                              const float* __restrict__ weight, uint32_t T,
@@ -349,31 +346,31 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_combine(s2r_mat rows, uint3
   const uint32_t t = __builtin_amdgcn_readfirstlane(blockIdx.x / spans * kMoeWaves + threadIdx.x / 64);
   if (t >= T) return;
   const Choices of(place, weight, t, K, R);
-  const uint32_t c = span * (kCombinePieces * 512) + lane * 8;
+  const uint32_t c = span * (PIECES * 512) + lane * 8;
   const uint64_t ld = rows.ld * elem_bytes<DT>();
-  float sum[kCombinePieces][8] = {};
-  for (uint32_t k0 = 0; k0 < K; k0 += kCombineRows) {
-    float v[kCombineRows][kCombinePieces][8];
+  float sum[PIECES][8] = {};
+  for (uint32_t k0 = 0; k0 < K; k0 += ROWS) {
+    float v[ROWS][PIECES][8];
 #pragma unroll
-    for (int j = 0; j < kCombineRows; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
       const uint32_t row = k0 + j < K ? of.row_of(k0 + j) : ~0u;
       if (row == ~0u) continue;
       const uint8_t* from = static_cast<const uint8_t*>(rows.data) + (uint64_t)row * ld;
 #pragma unroll
-      for (int u = 0; u < kCombinePieces; ++u) load8<DT>(from, c + 512 * u, D, v[j][u]);
+      for (int u = 0; u < PIECES; ++u) load8<DT>(from, c + 512 * u, D, v[j][u]);
     }
 #pragma unroll
-    for (int j = 0; j < kCombineRows; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
       if (k0 + j >= K || of.row_of(k0 + j) == ~0u) continue;  // the same for the wave
       const float w = of.weight_of(k0 + j);
 #pragma unroll
-      for (int u = 0; u < kCombinePieces; ++u)
+      for (int u = 0; u < PIECES; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[u][e] = __builtin_fmaf(w, v[j][u][e], sum[u][e]);
     }
   }
 #pragma unroll
-  for (int u = 0; u < kCombinePieces; ++u) {
+  for (int u = 0; u < PIECES; ++u) {
     const f32x4 lo = {sum[u][0], sum[u][1], sum[u][2], sum[u][3]}, hi = {sum[u][4], sum[u][5], sum[u][6], sum[u][7]};
     if (c + 512 * u < D) store8(y, t, c + 512 * u, D, lo, hi);
   }
@@ -382,15 +379,20 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_combine(s2r_mat rows, uint3
 hipError_t launch_moe_combine(uint64_t T, uint32_t K, uint64_t D, const s2r_mat& rows, uint64_t R,
                               const int32_t* place, const float* weight, const s2r_mat& y,
                               hipStream_t s) {
-  const uint64_t each = kCombinePieces * 512, spans = (D + each - 1) / each;
+  // 1024 columns to a wave, or 512 with more rows at once where that leaves compute units idle
+  const bool few = T * ((D + 1023) / 1024) < 16 * 256;
+  const uint64_t each = few ? 512 : 1024, spans = (D + each - 1) / each;
   trace_mark(s, "k_moe_combine");
   by_rows(T, kMoeWaves, spans, [&](uint64_t t, uint64_t n) {
     const s2r_mat to = from_row(y, t);
     const dim3 grid((uint32_t)(spans * ((n + kMoeWaves - 1) / kMoeWaves)));
-    S2R_MOE_TYPES(rows.dtype,
-                  hipLaunchKernelGGL((k_moe_combine<DT>), grid, dim3(kMoeThreads), 0, s, rows, (uint32_t)R,
-                                     place + t * K, weight ? weight + t * K : nullptr, (uint32_t)n, K,
-                                     (uint32_t)D, to, (uint32_t)spans));
+#define S2R_COMBINE(PIECES, ROWS)                                                                                  \
+  S2R_MOE_TYPES(rows.dtype, hipLaunchKernelGGL((k_moe_combine<DT, PIECES, ROWS>), grid, dim3(kMoeThreads), 0, s, rows, \
+                                               (uint32_t)R, place + t * K, weight ? weight + t * K : nullptr,      \
+                                               (uint32_t)n, K, (uint32_t)D, to, (uint32_t)spans))
+    if (few) S2R_COMBINE(1, 8);
+    else S2R_COMBINE(2, 4);
+#undef S2R_COMBINE
   });
   return hipGetLastError();
 }
