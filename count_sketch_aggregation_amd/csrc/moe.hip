@@ -9,9 +9,9 @@
 // whole lines wherever they lie, and no list of a row's token is needed.  Bound by HBM; measured on
 // MI355X, where a large copy moves 5.12 TB/s:
 //   gather 16384 x 4096 bf16, 4 choices, to 8 bits         81 us (5.0 TB/s)
-//   combine 8192 x 4096 bf16, 4 choices                    68 us (4.9)
+//   combine 8192 x 4096 bf16, 4 choices                    68 us (4.9); 1001 x 1000 fp16, 6 choices 6.0
 //   its gradient to 8 bits, with that of the weights       90 us (5.2)
-//   route 65536 choices among 64                           10 us in two launches, 192 choices 3.6 in one
+//   route 65536 choices among 64                           7 us in two launches, 192 choices 2.9 in one
 #include "moe_launch.hpp"
 #include "q8_device.hpp"
 #include "s2r_device.hpp"
@@ -24,13 +24,16 @@ namespace s2r {
 // each workgroup of the second adds up those before its own: integers, the same in any order.
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
-constexpr uint64_t kRouteChunk = 2048;   // at least
+constexpr uint64_t kRouteChunk = 2048;   // at least, of several
+constexpr uint64_t kRouteAlone = 4096;   // choices up to which one workgroup takes them all
 constexpr uint64_t kRouteChunks = 256;   // at most: one for every compute unit
 
 struct RouteCut {
   uint32_t chunk, chunks;
 };
+// 192 choices take 2.9 us, 2000 4.1, 4096 5.7 (6.3 in two chunks), 65536 7.0.
 inline RouteCut route_cut(uint64_t A) {
+  if (A <= kRouteAlone) return {A <= 1024 ? 1024u : A <= 2048 ? 2048u : 4096u, 1};
   uint64_t chunk = (A + kRouteChunks - 1) / kRouteChunks;
   chunk = (chunk + kRouteThreads - 1) / kRouteThreads * kRouteThreads;
   if (chunk < kRouteChunk) chunk = kRouteChunk;

@@ -62,7 +62,7 @@ def route(expert, E):
 
 
 ROUTES = [(0, 1, 1), (1, 1, 1), (1, 8, 64), (3, 2, 5), (24, 8, 64), (64, 1, 3), (257, 4, 17), (683, 3, 129), (1024, 2, 1024),
-          (2049, 1, 128), (1000, 7, 128), (5000, 8, 200), (4096, 64, 60), (300000, 2, 1000), (70001, 8, 31)]
+          (2049, 1, 128), (1024, 1, 7), (4096, 1, 40), (4097, 1, 40), (1366, 3, 1), (1000, 7, 128), (5000, 8, 200), (4096, 64, 60), (300000, 2, 1000), (70001, 8, 31)]
 
 
 @pytest.mark.parametrize("T,K,E", ROUTES)
