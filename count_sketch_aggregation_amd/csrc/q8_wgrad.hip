@@ -421,15 +421,18 @@ void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8
                      (uint32_t)N, (uint32_t)K, accumulate);
 }
 
-// Tiles of 256 where they fill the GPU, else of 128, two to a compute unit.  An expert's sum is not cut, for there
-// are as many sums as experts; with one or two experts and small matrices a long sum is bound by its own
-// blocks, 0.9 us for 64 rows (two halves beside each other on one compute unit took 0.87 as long).
+// Tiles of 256 where they fill the GPU twice, for the longest sums take a tile's time each (8000 tokens of 2
+// choices, 16 experts of 1024 x 1024: 116 us in 256 of them, 78 in tiles of 128; 2000 of 4, 32 experts: 52 in
+// 512, and 56).  Else of 128 of eight waves, two to a compute unit (of four waves: 4000 tokens of 4 choices, 16
+// experts of 1000 x 516 49 us, 44 with eight; 4186 of 2, 2 of 350 x 182 61 and 50).  An expert's sum is not cut,
+// for there are as many sums as experts; with one or two experts and small matrices a long sum is bound by
+// its own blocks, 0.7 us for 64 rows.
 template <int KY, int FX>
 void go_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, const s2r_mat& d,
                       const s2r_q8_mat& q, const s2r_q8_mat& x, float* dw, uint64_t lddw, uint64_t dw_step,
                       bool accumulate, hipStream_t s) {
   auto tiles = [&](uint64_t n, uint64_t side) { return (uint32_t)((n + side - 1) / side); };
-  const bool large = (uint64_t)tiles(N, 256) * tiles(K, 256) * e.experts >= kTileCus;
+  const bool large = (uint64_t)tiles(N, 256) * tiles(K, 256) * e.experts >= 2 * kTileCus;
   const uint32_t side = large ? 256 : 128, nt = tiles(N, side), kt = tiles(K, side);
   // a launch holds below 2^32 threads
   const uint32_t most = std::max<uint64_t>(1, ((1ull << 32) - 1) / ((uint64_t)nt * kt * 512));
@@ -441,7 +444,7 @@ void go_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, 
       hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 4, 4, 2, true>), grid, dim3(512), 0, s, d, q, x, dw + i * dw_step,
                          lddw, dw_step, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, 0, of);
     else
-      hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 2, 2, 2, 2, true>), grid, dim3(256), 0, s, d, q, x, dw + i * dw_step,
+      hipLaunchKernelGGL((k_q8_wgrad<KY, FX, 4, 2, 1, 2, true>), grid, dim3(512), 0, s, d, q, x, dw + i * dw_step,
                          lddw, dw_step, (uint32_t)M, (uint32_t)N, (uint32_t)K, accumulate, nt, kt, 0, of);
   }
 }

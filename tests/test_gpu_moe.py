@@ -311,7 +311,9 @@ def wgrad(m, N, K, dy, x, dw0=None, lddw=None, gap=0, off=0):
 
 
 WGRADS = [(1, 1, 1, 1, 1), (3, 2, 4, 40, 70), (100, 2, 3, 130, 200), (300, 4, 40, 257, 65), (1501, 2, 8, 500, 258), (900, 4, 5, 300, 2100),
-          (3000, 2, 70, 300, 520)]
+          (3000, 2, 70, 300, 520),
+          # 256 x 256 tiles, of many experts and of few
+          (1500, 2, 130, 300, 260), (600, 2, 30, 1100, 1000)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
