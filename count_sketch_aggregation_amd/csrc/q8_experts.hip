@@ -103,16 +103,18 @@ namespace {
 
 // A few rows to an expert are summed as few rows are, more go to tiles; the host knows only how many there are on
 // average (M is at most 20 for each: 100 tokens of 4 choices, 32 experts of 2048 x 2048 38 us, 41 in tiles; 200
-// tokens 57 and 38).
+// tokens 57 and 38; or 64 for each where there would be few tiles: 100 tokens of 2 choices, 8 experts of 1024 x 1024 8.5
+// us, 12.3 in tiles; 300 tokens, of 512 x 1024 18.0 and 12.0).
 template <int FA, int FB>
 void go_gemm_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, const s2r_q8_mat& a,
                      const s2r_q8_mat& b, ExpertSteps steps, const s2r_mat& c, hipStream_t s) {
   const uint32_t m = (uint32_t)M, n = (uint32_t)N, k = (uint32_t)K;
-  if (M <= 20 * (uint64_t)e.experts) {
-    // experts with rows are at least 4 rows apart
-    const uint32_t some = (uint32_t)std::min<uint64_t>(e.experts, (M + 3) / 4);
+  const uint64_t some = std::min<uint64_t>(e.experts, (M + 3) / 4);  // experts with rows are at least 4 rows apart
+  auto tiles = [&](uint64_t side) { return (M / side + some) * ((N + side - 1) / side); };
+  const uint64_t few = tiles(128) <= kTileCus / 2 ? 64 : 20;
+  if (M <= few * e.experts) {
     trace_mark(s, "k_q8_gemm_few_experts");
-    const dim3 grid((n + 31) / 32, some);
+    const dim3 grid((n + 31) / 32, (uint32_t)some);
     // two workgroups for every compute unit or fewer: more waves each (2 experts of 4096 x 4096, one token: 10 us
     // with 8, 13 with 4; 60 of 2048 x 2048, 64 tokens: 65 and 56)
     if ((uint64_t)grid.x * some <= 2 * kTileCus)
@@ -127,8 +129,6 @@ void go_gemm_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, c
   // tiles are reckoned with as there can be, for some experts have many more rows than others (4000 tokens of one
   // choice, 32 experts of 2048 x 1024: 53 and 33).
   const uint32_t blocks = (k + kQ8Block - 1) / kQ8Block;
-  const uint64_t some = std::min<uint64_t>(e.experts, M / 4);
-  auto tiles = [&](uint64_t side) { return (M / side + some) * ((N + side - 1) / side); };
   auto rounds = [](uint64_t n, uint64_t width) { return (n + width - 1) / width; };
   const bool large = rounds(tiles(256), kTileCus) * (blocks * 2700 + 8000) < rounds(tiles(128), 2 * kTileCus) * (blocks * 1500 + 4500);
   const dim3 grid((uint32_t)(large ? std::min<uint64_t>(tiles(256), kTileCus) : std::min<uint64_t>(tiles(128), 2 * kTileCus)));
