@@ -1,4 +1,4 @@
-// q8_tile.hpp -- what the two tiled products share: direct loads to LDS, barriers, the order
+// q8_tile.hpp -- what the tiled products share: direct loads to LDS, barriers, the order
 // of tiles over the chip and the sum of partial results (internal to libs2r).
 #pragma once
 
