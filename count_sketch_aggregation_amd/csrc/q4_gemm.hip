@@ -437,7 +437,7 @@ hipError_t launch_q4_gemm(uint64_t M, uint64_t N, uint64_t K, const s2r_q4_mat& 
 #define S2R_TILE(F, TAIL)                                                                                      \
   hipLaunchKernelGGL((k_q4_gemm<2, 2, F, F, TAIL>), grid, dim3(256), 0, s, a, b, out, part_bytes, m, n, k, p.mt, \
                      p.nt, total, 2 * p.cut.blocks)
-  trace_mark(s, "k_q4_gemm");
+  trace_mark(s, p.side == 256 ? "k_q4_gemm<256>" : "k_q4_gemm<128>");
   const bool tail = k % kQ4Chunk != 0;
   if (p.side == 256 && tail) S2R_TILE(4, true);
   else if (p.side == 256) S2R_TILE(4, false);
