@@ -212,8 +212,10 @@ def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    # the current stream's handle without a Stream object around it, which costs as much as a short call
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the current stream's handle without a Stream object around it, which costs as much as a short call,
+    # where this torch has such a call: it is none of its public ones
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
 
 
 # ---------------------------------------------------------------------------------------
