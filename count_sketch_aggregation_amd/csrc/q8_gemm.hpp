@@ -66,6 +66,18 @@ struct ExpertTiles {
   s2r_experts of;
   ExpertSteps steps;
 };
+// Tiles up to and with each expert, and those of each wave's experts: LDS that is there only where it is asked for, for
+// the plain 256 x 256 form takes all there is.
+template <int WAVES>
+struct ExpertLds {
+  uint32_t upto[S2R_MAX_EXPERTS], wave[WAVES];
+};
+template <int WAVES>
+__device__ inline ExpertLds<WAVES>& expert_lds() {
+  __shared__ ExpertLds<WAVES> x;
+  return x;
+}
+constexpr int kLdsBytes = 160 * 1024;  // of a compute unit
 template <int FA, int FB, int WM, int WN, int FM, int FN, bool TAIL, bool WIDE, bool EXPERTS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     s2r_q8_mat a, s2r_q8_mat b, s2r_mat c, uint64_t part_bytes, uint32_t M, uint32_t N, uint32_t K,
@@ -76,14 +88,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
   static_assert(kLoads - kLoads * 5 / 8 <= FM * FN, "late loads have a slot each");
   constexpr int kTurnRows = kWaves > 4 ? 16 : 32, kTurn = kTurnRows * 64 * 4;  // a wave's results in LDS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBytes + (EXPERTS ? 0 : kWaves * kTurn)];
-  __shared__ uint32_t tiles_to[EXPERTS ? S2R_MAX_EXPERTS : 1], wave_tiles[kWaves];
+  static_assert(sizeof(lds) + (EXPERTS ? sizeof(ExpertLds<kWaves>) : 0) <= kLdsBytes, "");
 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
   const uint32_t wm = wave / WN * (32 * FM), wn = wave % WN * (32 * FN);
   const uint32_t blocks = (K + kQ8Block - 1) / kQ8Block;
 
-  if (EXPERTS) {
+  if constexpr (EXPERTS) {
+    ExpertLds<kWaves>& tiles = expert_lds<kWaves>();
     constexpr uint32_t kEach = S2R_MAX_EXPERTS / (64 * kWaves);  // experts of a thread
     uint32_t mine[kEach], sum = 0;
 #pragma unroll
@@ -100,16 +113,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
       const uint32_t v = (uint32_t)__shfl_up((int)upto, o);
       if (lane >= o) upto += v;
     }
-    if (lane == 63) wave_tiles[wave] = upto;
+    if (lane == 63) tiles.wave[wave] = upto;
     __syncthreads();
     m_tiles = 0;
     uint32_t before = upto - sum;
     for (uint32_t w = 0; w < kWaves; ++w) {
-      if (w < wave) before += wave_tiles[w];
-      m_tiles += wave_tiles[w];
+      if (w < wave) before += tiles.wave[w];
+      m_tiles += tiles.wave[w];
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) tiles_to[threadIdx.x * kEach + i] = before + mine[i];
+    for (uint32_t i = 0; i < kEach; ++i) tiles.upto[threadIdx.x * kEach + i] = before + mine[i];
     m_tiles = __builtin_amdgcn_readfirstlane(m_tiles);
     total = m_tiles * n_tiles;
     __syncthreads();
@@ -120,14 +133,18 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_q8_gemm(
     uint32_t m0, end, expert;
   };
   auto row_of = [&](uint32_t tile) {
-    if (!EXPERTS) return RowOf{tile * TM, M, 0};
-    uint32_t e = 0;  // experts whose tiles end at or before this one
-    for (uint32_t i = 0; i < experts.of.experts; i += 64)
-      e += (uint32_t)__popcll(__ballot(i + lane < experts.of.experts && tiles_to[i + lane] <= tile));
-    e = __builtin_amdgcn_readfirstlane(e);
-    const uint32_t first = min(experts.of.first[e], M), rows = min(experts.of.rows[e], M - first);
-    const uint32_t m0 = first + (tile - (e ? tiles_to[e - 1] : 0)) * TM;
-    return RowOf{(uint32_t)__builtin_amdgcn_readfirstlane(m0), (uint32_t)__builtin_amdgcn_readfirstlane(first + rows), e};
+    if constexpr (EXPERTS) {
+      const uint32_t* const upto = expert_lds<kWaves>().upto;
+      uint32_t e = 0;  // experts whose tiles end at or before this one
+      for (uint32_t i = 0; i < experts.of.experts; i += 64)
+        e += (uint32_t)__popcll(__ballot(i + lane < experts.of.experts && upto[i + lane] <= tile));
+      e = __builtin_amdgcn_readfirstlane(e);
+      const uint32_t first = min(experts.of.first[e], M), rows = min(experts.of.rows[e], M - first);
+      const uint32_t m0 = first + (tile - (e ? upto[e - 1] : 0)) * TM;
+      return RowOf{(uint32_t)__builtin_amdgcn_readfirstlane(m0), (uint32_t)__builtin_amdgcn_readfirstlane(first + rows), e};
+    } else {
+      return RowOf{tile * TM, M, 0};
+    }
   };
 
   // where this lane's pieces of a block come from, relative to the tile's first row
