@@ -484,7 +484,8 @@ def _floats(t, shape: tuple, where: str):
 
 
 def experts(first, rows) -> s2r_experts:
-    """Descriptor of the experts' rows, two int32 tensors [E]; keeps them alive."""
+    """Descriptor of the experts' rows, two int32 tensors [E]; keeps them alive.  Every element of `first` is a
+    multiple of 4: nothing on the host can see whether it is, and scales of other rows may be taken where it is not."""
     E = rows.numel()
     e = s2r_experts(_ints(first, (E,), "experts"), _ints(rows, (E,), "experts"), E)
     e.tensors = first, rows

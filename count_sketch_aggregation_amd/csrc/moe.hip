@@ -7,11 +7,12 @@
 //
 // Everything goes by tokens and not by rows: a token is read (or written) once, its K rows are
 // whole lines wherever they lie, and no list of a row's token is needed.  Bound by HBM; measured on
-// MI355X, where a large copy moves 5.12 TB/s:
-//   gather 16384 x 4096 bf16, 4 choices, to 8 bits         81 us (5.0 TB/s)
+// MI355X, where a large copy moves 5.18 TB/s:
+//   gather 16384 x 4096 bf16, 4 choices, to 8 bits         81 us (5.0 TB/s); as it is 129 (5.2), both 210
 //   combine 8192 x 4096 bf16, 4 choices                    68 us (4.9); 1001 x 1000 fp16, 6 choices 6.0
-//   its gradient to 8 bits, with that of the weights       90 us (5.2)
-//   route 65536 choices among 64                           7 us in two launches, 192 choices 2.9 in one
+//   its gradient to 8 bits, with that of the weights       89 us (5.2); to bf16 116 (5.2), of fp32 to fp32 247 (4.9)
+//   route 65536 choices among 64                           two launches of 4.8 us in a trace, 7.0 a call among others
+//                                                          in a graph; 192 choices 2.8 and 3.0 in one launch
 #include "moe_launch.hpp"
 #include "q8_device.hpp"
 #include "s2r_device.hpp"
@@ -31,7 +32,7 @@ constexpr uint64_t kRouteChunks = 256;   // at most: one for every compute unit
 struct RouteCut {
   uint32_t chunk, chunks;
 };
-// 192 choices take 2.9 us, 2000 4.1, 4096 5.7 (6.3 in two chunks), 65536 7.0.
+// A call among others in a graph: 192 choices take 3.0 us, 2000 4.1, 4096 5.7 (6.3 in two chunks), 65536 7.0.
 inline RouteCut route_cut(uint64_t A) {
   if (A <= kRouteAlone) return {A <= 1024 ? 1024u : A <= 2048 ? 2048u : 4096u, 1};
   uint64_t chunk = (A + kRouteChunks - 1) / kRouteChunks;

@@ -7,7 +7,7 @@
 // their scales.
 //
 // Measured on MI355X, 16384 x 8192 x 4096 to bf16: 272 to 298 us by card and values, 3.7 to 4.0 PFLOP/s (a
-// library's product of as many 4-bit codes 491, of 8-bit ones 442, of bf16 799); 4.5 with a sum of 8192, 6.0 if all
+// library's product of as many 4-bit codes 481, of 8-bit ones 359, of bf16 697); 4.5 with a sum of 8192, 6.0 if all
 // codes are zeros.  A chunk of 512 of a 256 x 256 tile takes 3.3 us, 2.6 for zeros, where its matrix
 // instructions take 4096 cycles: mostly power.  Results take 9 us a tile, in which all compute units write
 // at once: 268 MB, 45 us in all at the rate of a large fill.

@@ -2,9 +2,10 @@
 //
 // For each 32 elements of a row: a = the largest magnitude, scale = the least power of two with
 // a <= 6 scale, code = value / scale to nearest even.  The transpose has blocks of 32 rows of a column and so
-// scales and codes of its own; both are written from one read of x.  Bound by HBM.  Measured on MI355X, where a large
-// copy moves 5.12 TB/s: 8192 x 8192 bf16 and its transpose to 4 bits 64 us (4.3 TB/s), back to bf16 28 to 32
-// (5.3 and more); 1001 x 1000 fp32 3.1, and back to bf16 3.2.
+// scales and codes of its own; both are written from one read of x.  Measured on MI355X, where a large copy moves 5.18
+// TB/s: rows of 8192 x 8192 bf16 to 4 bits 34 us (5.0 TB/s), back to bf16 28 to 32 (5.3 and more): bound by HBM.  With the
+// transpose 52 us, 3.9 TB/s, and 64 (3.2) right behind two loads of 134 MB each: most likely since a tile leaves
+// half lines of the transpose's codes, and its scales as single bytes.  1001 x 1000 fp32 3.1, and back to bf16 3.2.
 #include "q4_device.hpp"
 #include "q4_launch.hpp"
 #include "q8_tile.hpp"

@@ -424,9 +424,9 @@ void go_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat& d, const s2r_q8
 // Tiles of 256 where they fill the GPU twice, for the longest sums take a tile's time each (8000 tokens of 2
 // choices, 16 experts of 1024 x 1024: 116 us in 256 of them, 78 in tiles of 128; 2000 of 4, 32 experts: 52 in
 // 512, and 56).  Else of 128 of eight waves, two to a compute unit (of four waves: 4000 tokens of 4 choices, 16
-// experts of 1000 x 516 49 us, 44 with eight; 4186 of 2, 2 of 350 x 182 61 and 50).  An expert's sum is not cut,
-// for there are as many sums as experts; with one or two experts and small matrices a long sum is bound by
-// its own blocks, 0.7 us for 64 rows.
+// experts of 1000 x 516 49 us, 44 with eight; 4186 of 2, 2 of 350 x 182 61 and 50).  An expert's sum is not cut:
+// where one expert has most of the rows and matrices are small, its sum is bound by its own blocks, 0.65 us for 64 rows
+// (32768 rows of one expert of 256 x 256: 330 us; of four 88).
 template <int KY, int FX>
 void go_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_experts& e, const s2r_mat& d,
                       const s2r_q8_mat& q, const s2r_q8_mat& x, float* dw, uint64_t lddw, uint64_t dw_step,
