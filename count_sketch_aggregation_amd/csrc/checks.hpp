@@ -50,6 +50,20 @@ inline bool sizes_ok(uint64_t a, uint64_t b, uint64_t c = 0) {
   return a < kMaxSize && b < kMaxSize && c < kMaxSize;
 }
 
+// Elements from the first of a matrix [rows][ld] of `cols` columns to behind its last, and of `count` of them `step`
+// apart (of `own` elements each) to behind the last one's; false where that, or its bytes, passes 64 bits: a stride like
+// -1 would wrap round to a small one.
+inline bool extent(uint64_t rows, uint64_t ld, uint64_t cols, uint64_t* n) {
+  *n = 0;
+  return rows == 0 || cols == 0 ||
+         (!__builtin_mul_overflow(rows - 1, ld, n) && !__builtin_add_overflow(*n, cols, n));
+}
+inline bool extent_ok(uint64_t count, uint64_t step, uint64_t own, uint64_t elem_size) {
+  uint64_t n = 0;
+  return own == 0 || ((count <= 1 || !__builtin_mul_overflow(count - 1, step, &n)) && !__builtin_add_overflow(n, own, &n) &&
+                      n <= UINT64_MAX / elem_size);
+}
+
 inline hipStream_t on(void* stream) { return static_cast<hipStream_t>(stream); }
 
 inline s2r_status done(hipError_t e, void* stream) {

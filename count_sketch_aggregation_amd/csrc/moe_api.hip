@@ -120,6 +120,11 @@ s2r_status s2r_q8_gemm_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_exp
   v.add(check(a, M, K, M));
   v.add(check(b, N, K, blocks128(N)));
   v.add(check(c, M, N));
+  uint64_t codes, scales;
+  if (!extent(N, b->ld, K, &codes) || !extent_ok(experts->experts, b_step, codes, 1) ||
+      !extent(blocks128(K), b->lds, blocks128(N), &scales) ||
+      !extent_ok(experts->experts, b_scale_step, scales, 1))
+    v.add(S2R_ERR_DIM);
   if (b_step % 16 != 0) v.add(S2R_ERR_ALIGN);
   if (v.st != S2R_OK) return v.st;
   if (M == 0 || N == 0) return S2R_OK;
@@ -135,7 +140,10 @@ s2r_status s2r_q8_wgrad_experts(uint64_t M, uint64_t N, uint64_t K, const s2r_ex
   if (N > 0 && K > 0 && !dw) return S2R_ERR_NULL;
   Verdict v;
   if (!sizes_ok(M, N, K) || (dy16 && dy8) || lddw < K) v.add(S2R_ERR_DIM);
-  if (N > 0 && experts->experts > 1 && dw_step < (N - 1) * lddw + K) v.add(S2R_ERR_DIM);
+  uint64_t own;
+  if (!extent(N, lddw, K, &own) || (experts->experts > 1 && dw_step < own) ||
+      !extent_ok(experts->experts, dw_step, own, sizeof(float)))
+    v.add(S2R_ERR_DIM);
   check_experts(v, experts);
   if (dy16) {
     v.add(check(dy16, M, N));

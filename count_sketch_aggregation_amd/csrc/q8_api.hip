@@ -93,6 +93,8 @@ s2r_status s2r_q8_wgrad(uint64_t M, uint64_t N, uint64_t K, const s2r_mat* dy16,
   if (N > 0 && K > 0 && !dw) return S2R_ERR_NULL;
   Verdict v;
   if (!sizes_ok(M, N, K) || (dy16 && dy8) || lddw < K) v.add(S2R_ERR_DIM);
+  uint64_t own;
+  if (!extent(N, lddw, K, &own) || !extent_ok(1, 0, own, sizeof(float))) v.add(S2R_ERR_DIM);
   if (dy16) {
     v.add(check(dy16, M, N));
     if (dy16->dtype != S2R_BF16) v.add(S2R_ERR_DIM);

@@ -28,6 +28,7 @@
  * fp32 in an order that the sizes and rows fix, and errors.  Beyond them:
  *   - E is 1 .. 1024 and K 1 .. 64, T * K below 2^27 (S2R_ERR_DIM otherwise).
  *   - first, rows, expert, place, weight and dweight are 4-byte aligned.
+ *   - Steps from one expert to the next reach no further than 64 bits of bytes (S2R_ERR_DIM otherwise).
  */
 #ifndef S2R_MOE_H
 #define S2R_MOE_H
